@@ -1,0 +1,354 @@
+// moe_grad.cu -- the expert sort of unquantised rows, its gradient, and the
+// gradient of the weighted combine, sm_100a.
+//
+//   permute            xs[pos[r]] = x[r / topk], padding rows zero
+//   permute backward   dx[t] = sum_k dxs[pos[t topk + k]]
+//   combine backward   of out[t] = sum_k w[r] D[pos[r]]:
+//                      dD[pos[r]] = w[r] dout[t], dw[r] = <dout[t], D[pos[r]]>
+//
+// All three are HBM-bound streams.  A CTA takes a token: its row of x or dout
+// is read once for all of its slots, and every row of the layout is touched
+// once.  Positions are checked against the layout's rows before any access; a
+// position outside is flagged and its slot skipped.
+//
+// Padding rows.  The rows of a used block (one that holds a routed row) that
+// no slot fills are set to zero by CTAs of their own in the same launch: each
+// takes a run of blocks, marks the rows that pos names in a bitmap in shared
+// memory, and zeroes the rest.  Reading pos (4 bytes a slot) once per such CTA
+// costs little next to the rows, and saves the workspace, the launches and
+// the atomics on memory that a map from rows to slots would need.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "fp8gemm.h"
+#include "moe_layout.cuh"
+#include "quant_impl.cuh"
+#include "rows.cuh"
+
+namespace {
+
+using namespace fp8g::rows;
+using fp8g::moe::kMaxExperts;
+using fp8g::moe::kMaxTopk;
+
+constexpr int kPadBlocks = 256;  // most blocks of a padding CTA: its bitmap is 4 KB
+
+// pos[r] if it names a row of the layout, -1 if the slot is dropped; anything
+// else is flagged and treated as dropped.
+__device__ __forceinline__ int checked_pos(const int32_t* pos, long r, int M, uint32_t* err) {
+  const int p = __ldg(pos + r);
+  if (p >= -1 && p < M) return p;
+  atomicOr(err, FP8G_DEVERR_BAD_POS);
+  return -1;
+}
+
+// Calls zero_row(row) for the rows of blocks [b0, b1) that no slot fills, in
+// blocks with at least one filled row.  All threads of the CTA call it; each
+// warp takes every blockDim / 32-th row.
+template <typename ZeroRow>
+__device__ __forceinline__ void pad_blocks(const int32_t* __restrict__ pos, long R, int b0, int b1, uint32_t* bits,
+                                           uint32_t* err, ZeroRow zero_row) {
+  const int words = (b1 - b0) * 4;
+  for (int i = threadIdx.x; i < words; i += blockDim.x) bits[i] = 0u;
+  __syncthreads();
+  const int lo = b0 * 128, n = (b1 - b0) * 128;
+  auto mark = [&](int p) {
+    const uint32_t i = static_cast<uint32_t>(p - lo);
+    if (i < static_cast<uint32_t>(n) && (atomicOr(&bits[i >> 5], 1u << (i & 31)) >> (i & 31) & 1u))
+      atomicOr(err, FP8G_DEVERR_BAD_POS);  // two slots in one row
+  };
+  long r = threadIdx.x;
+  for (; r + 7L * blockDim.x < R; r += 8L * blockDim.x) {
+    int p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = __ldg(pos + r + static_cast<long>(i) * blockDim.x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mark(p[i]);
+  }
+  for (; r < R; r += blockDim.x) mark(__ldg(pos + r));
+  __syncthreads();
+  const int w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  for (int i = w; i < n; i += nw) {
+    const uint32_t* blk = bits + (i >> 7) * 4;
+    if (!(blk[0] | blk[1] | blk[2] | blk[3])) continue;  // an unused block
+    if (bits[i >> 5] >> (i & 31) & 1u) continue;
+    zero_row(static_cast<long>(lo + i));
+  }
+}
+
+// ---------------------------------------------------------------- permute
+// CTAs [0, pads) zero padding rows; the others take a token each.  Rows are
+// moved as 16-byte vectors, whatever their type.
+template <int kCap>
+__global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int T, int topk,
+                                                          const int32_t* __restrict__ pos, uint4* __restrict__ xs, int M,
+                                                          int blocks, int pads, uint32_t* err) {
+  __shared__ uint32_t bits[kPadBlocks * 4];
+  if (static_cast<int>(blockIdx.x) < pads) {
+    const int per = (blocks + pads - 1) / pads;
+    const int b0 = min(blocks, static_cast<int>(blockIdx.x) * per), b1 = min(blocks, b0 + per);
+    pad_blocks(pos, static_cast<long>(T) * topk, b0, b1, bits, err, [&](long row) {
+      for (int i = threadIdx.x & 31; i < vecs; i += 32) __stcs(xs + row * vecs + i, make_uint4(0u, 0u, 0u, 0u));
+    });
+    return;
+  }
+  for (long t = static_cast<long>(blockIdx.x) - pads; t < T; t += static_cast<long>(gridDim.x) - pads) {
+    int p[kCap];
+#pragma unroll
+    for (int k = 0; k < kCap; ++k) p[k] = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+    for (int j = threadIdx.x; j < vecs; j += blockDim.x) {
+      const uint4 v = __ldcs(x + t * vecs + j);
+#pragma unroll
+      for (int k = 0; k < kCap; ++k)
+        if (p[k] >= 0) __stcs(xs + static_cast<long>(p[k]) * vecs + j, v);
+    }
+  }
+}
+
+template <bool kF32, int kCap>
+__global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* __restrict__ dxs, int N,
+                                                                   const int32_t* __restrict__ pos, int T, int topk,
+                                                                   void* __restrict__ dx, int M, uint32_t* err) {
+  for (long t = blockIdx.x; t < T; t += gridDim.x) {
+    int p[kCap];
+#pragma unroll
+    for (int k = 0; k < kCap; ++k) p[k] = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+    for (int j = threadIdx.x; j < N / 8; j += blockDim.x) {
+      Raw8<kF32> v[kCap];
+#pragma unroll
+      for (int k = 0; k < kCap; ++k)
+        v[k] = p[k] >= 0 ? load8<kF32>(dxs, static_cast<long>(p[k]) * N + 8 * j) : zero8<kF32>();
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kCap; ++k) {
+        float f[8];
+        unpack8<kF32>(v[k], f);
+        if (p[k] >= 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] += f[i];
+        }
+      }
+      store8<kF32>(dx, t * N + 8 * j, acc);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- combine backward
+// kQuant: the rows leave as e4m3 codes and 1x128 scales (16 lanes hold a
+// group).  The group's largest |w x| is |w| times its largest |x|, rounded
+// once: rounding is monotonic, so one reduction over x serves every slot.
+template <bool kQuant, int kCap>
+__global__ void __launch_bounds__(256) moe_combine_backward_kernel(const uint16_t* __restrict__ dout,
+                                                                   const uint16_t* __restrict__ D, int N,
+                                                                   const int32_t* __restrict__ pos,
+                                                                   const float* __restrict__ w, int T, int topk,
+                                                                   uint16_t* __restrict__ dD, uint8_t* __restrict__ q,
+                                                                   float* __restrict__ sa, int ld_sa,
+                                                                   float* __restrict__ dw, int M, int blocks, int pads,
+                                                                   uint32_t* err) {
+  __shared__ uint32_t bits[kPadBlocks * 4];
+  __shared__ float s_dot[8][kCap];
+  if (static_cast<int>(blockIdx.x) < pads) {
+    const int per = (blocks + pads - 1) / pads;
+    const int b0 = min(blocks, static_cast<int>(blockIdx.x) * per), b1 = min(blocks, b0 + per);
+    pad_blocks(pos, static_cast<long>(T) * topk, b0, b1, bits, err, [&](long row) {
+      const int lane = threadIdx.x & 31;
+      uint4* out = kQuant ? reinterpret_cast<uint4*>(q + row * N) : reinterpret_cast<uint4*>(dD + row * N);
+      for (int i = lane; i < (kQuant ? N / 16 : N / 8); i += 32) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
+      if constexpr (kQuant)
+        for (int kb = lane; kb < N / 128; kb += 32) sa[static_cast<long>(kb) * ld_sa + row] = 0.f;
+    });
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_row = N / 8;
+  for (long t = static_cast<long>(blockIdx.x) - pads; t < T; t += static_cast<long>(gridDim.x) - pads) {
+    int p[kCap];
+    float wk[kCap], dot[kCap];
+#pragma unroll
+    for (int k = 0; k < kCap; ++k) {
+      p[k] = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+      wk[k] = k < topk && w ? __ldg(w + t * topk + k) : 1.f;
+      dot[k] = 0.f;
+    }
+    // every thread of a warp takes part in the group maxima
+    for (int j0 = 0; j0 < per_row; j0 += blockDim.x) {
+      const int j = j0 + threadIdx.x;
+      const bool in = j < per_row;
+      const Raw8<false> raw = in ? load8<false>(dout, t * N + 8L * j) : zero8<false>();
+      Raw8<false> v[kCap];
+      if (dw) {
+#pragma unroll
+        for (int k = 0; k < kCap; ++k)
+          v[k] = in && p[k] >= 0 ? load8<false>(D, static_cast<long>(p[k]) * N + 8L * j) : zero8<false>();
+      }
+      float g[8];
+      unpack8<false>(raw, g);
+      float amax = 0.f;
+      if constexpr (kQuant) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(g[i]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      }
+#pragma unroll
+      for (int k = 0; k < kCap; ++k) {
+        if (p[k] < 0 || !in) continue;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = wk[k] * g[i];
+        if constexpr (kQuant) {
+          const float sc = fp8g::quant::scale_of(fabsf(wk[k]) * amax);
+          uint32_t c[2];
+          fp8g::quant::encode_group(o, sc, c);
+          fp8g::quant::store_code_words(q + static_cast<long>(p[k]) * N + 8L * j, c);
+          if ((j & 15) == 0) sa[static_cast<long>(j >> 4) * ld_sa + p[k]] = sc;
+        } else {
+          store8<false>(dD, static_cast<long>(p[k]) * N + 8L * j, o);
+        }
+        if (dw) {
+          float d[8];
+          unpack8<false>(v[k], d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[k] = fmaf(g[i], d[i], dot[k]);
+        }
+      }
+    }
+    if (dw) {
+#pragma unroll
+      for (int k = 0; k < kCap; ++k) {
+        if (k >= topk) continue;
+        const float sum = warp_sum(dot[k]);
+        if (lane == 0) s_dot[warp][k] = sum;
+      }
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < topk) {
+        float sum = 0.f;
+        for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) sum += s_dot[i][threadIdx.x];
+        dw[t * topk + threadIdx.x] = sum;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// CTAs that zero padding rows: one per SM, or one per block, or enough for
+// their bitmaps.
+int pad_ctas(int blocks, int sms) {
+  return std::max((blocks + kPadBlocks - 1) / kPadBlocks, std::min(blocks, sms));
+}
+
+// The kernel for a compile-time bound on topk: 4, 8 or 16.
+template <typename F4, typename F8, typename F16>
+void by_topk(int topk, F4 f4, F8 f8, F16 f16) {
+  if (topk <= 4) f4();
+  else if (topk <= 8) f8();
+  else f16();
+}
+
+int row_threads(long vecs) { return static_cast<int>(std::min<long>(256, std::max<long>(32, (vecs + 31) / 32 * 32))); }
+
+int check_slots(int T, int topk, int N) {
+  if (T < 0 || topk < 1 || topk > kMaxTopk || N < 1 || static_cast<long>(T) * topk > 0x7FFFFFFFL)
+    return FP8G_ERR_INVALID_ARG;
+  return FP8G_OK;
+}
+
+}  // namespace
+
+extern "C" int fp8g_moe_permute(const void* x, int x_dtype, int T, int N, const int32_t* expert, int topk, int G,
+                                int blocks, void* xs, int32_t* pos, int32_t* m_indices, cudaStream_t stream) {
+  if (x_dtype != FP8G_IN_BF16 && x_dtype != FP8G_IN_F32) return FP8G_ERR_INVALID_ARG;
+  int rc = check_slots(T, topk, N);
+  if (rc) return rc;
+  if (G < 1 || G > kMaxExperts) return FP8G_ERR_INVALID_ARG;
+  const long R = static_cast<long>(T) * topk;
+  if (blocks < (R + 127) / 128 + G || blocks > 0x7FFFFFFF / 128) return FP8G_ERR_INVALID_ARG;
+  if (N % 8 != 0) return FP8G_ERR_MISALIGNED;
+  if (!m_indices || (R > 0 && (!x || !expert || !xs || !pos))) return FP8G_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(expert, 4) || !aligned(pos, 4) || !aligned(m_indices, 4))
+    return FP8G_ERR_MISALIGNED;
+  const int sms = sm_count();
+  uint32_t* err = fp8g::device_error_word();
+  if (sms <= 0 || !err) return FP8G_ERR_CUDA;
+  if (fp8g::moe::launch_layout<false>(expert, static_cast<int>(R), G, 0, pos, m_indices, blocks, err, stream) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return FP8G_ERR_CUDA;
+  }
+  if (R == 0) return FP8G_OK;
+  const long vecs = static_cast<long>(N) * (x_dtype == FP8G_IN_F32 ? 4 : 2) / 16;
+  if (vecs > 0x7FFFFFFFL) return FP8G_ERR_INVALID_ARG;
+  const int pads = pad_ctas(blocks, sms);
+  const unsigned grid = static_cast<unsigned>(pads + std::min<long>(T, 32L * sms));
+  auto go = [&](auto kernel) {
+    kernel<<<grid, row_threads(vecs), 0, stream>>>(static_cast<const uint4*>(x), static_cast<int>(vecs), T, topk, pos,
+                                                   static_cast<uint4*>(xs), blocks * 128, blocks, pads, err);
+  };
+  by_topk(topk, [&] { go(moe_permute_kernel<4>); }, [&] { go(moe_permute_kernel<8>); },
+          [&] { go(moe_permute_kernel<kMaxTopk>); });
+  if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
+  return FP8G_OK;
+}
+
+extern "C" int fp8g_moe_permute_backward(const void* dxs, int dtype, int blocks, int N, const int32_t* pos, int T,
+                                         int topk, void* dx, cudaStream_t stream) {
+  if (dtype != FP8G_IN_BF16 && dtype != FP8G_IN_F32) return FP8G_ERR_INVALID_ARG;
+  int rc = check_slots(T, topk, N);
+  if (rc) return rc;
+  if (blocks < 0 || blocks > 0x7FFFFFFF / 128) return FP8G_ERR_INVALID_ARG;
+  if (N % 8 != 0) return FP8G_ERR_MISALIGNED;
+  if (T == 0) return FP8G_OK;
+  if ((blocks > 0 && !dxs) || !pos || !dx) return FP8G_ERR_INVALID_ARG;
+  if (!aligned(dxs, 16) || !aligned(dx, 16) || !aligned(pos, 4)) return FP8G_ERR_MISALIGNED;
+  const int sms = sm_count();
+  uint32_t* err = fp8g::device_error_word();
+  if (sms <= 0 || !err) return FP8G_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(std::min<long>(T, 32L * sms));
+  auto go = [&](auto kernel) {
+    kernel<<<grid, row_threads(N / 8), 0, stream>>>(dxs, N, pos, T, topk, dx, blocks * 128, err);
+  };
+  if (dtype == FP8G_IN_F32)
+    by_topk(topk, [&] { go(moe_permute_backward_kernel<true, 4>); }, [&] { go(moe_permute_backward_kernel<true, 8>); },
+            [&] { go(moe_permute_backward_kernel<true, kMaxTopk>); });
+  else
+    by_topk(topk, [&] { go(moe_permute_backward_kernel<false, 4>); }, [&] { go(moe_permute_backward_kernel<false, 8>); },
+            [&] { go(moe_permute_backward_kernel<false, kMaxTopk>); });
+  if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
+  return FP8G_OK;
+}
+
+extern "C" int fp8g_moe_combine_backward(const uint16_t* dout, const uint16_t* D, int N, const int32_t* pos,
+                                         const float* w, int T, int topk, int blocks, uint16_t* dD, uint8_t* q,
+                                         float* sa, int ld_sa, float* dw, cudaStream_t stream) {
+  int rc = check_slots(T, topk, N);
+  if (rc) return rc;
+  if (blocks < 0 || blocks > 0x7FFFFFFF / 128) return FP8G_ERR_INVALID_ARG;
+  if (q && (N % 128 != 0 || ld_sa < blocks * 128L)) return FP8G_ERR_INVALID_ARG;
+  if (N % 8 != 0 || (q && ld_sa % 4 != 0)) return FP8G_ERR_MISALIGNED;
+  if (T == 0) return FP8G_OK;
+  if (!dout || !pos || (blocks > 0 && ((dD != nullptr) == (q != nullptr) || (q && !sa) || (dw && !D))))
+    return FP8G_ERR_INVALID_ARG;
+  if (!aligned(dout, 16) || !aligned(D, 16) || !aligned(dD, 16) || !aligned(q, 16) || !aligned(sa, 16) ||
+      !aligned(pos, 4) || !aligned(w, 4) || !aligned(dw, 4))
+    return FP8G_ERR_MISALIGNED;
+  const int sms = sm_count();
+  uint32_t* err = fp8g::device_error_word();
+  if (sms <= 0 || !err) return FP8G_ERR_CUDA;
+  const int pads = pad_ctas(blocks, sms);
+  const unsigned grid = static_cast<unsigned>(pads + std::min<long>(T, 32L * sms));
+  auto go = [&](auto kernel) {
+    kernel<<<grid, row_threads(N / 8), 0, stream>>>(dout, D, N, pos, w, T, topk, dD, q, sa, ld_sa, dw, blocks * 128,
+                                                    blocks, pads, err);
+  };
+  if (q)
+    by_topk(topk, [&] { go(moe_combine_backward_kernel<true, 4>); }, [&] { go(moe_combine_backward_kernel<true, 8>); },
+            [&] { go(moe_combine_backward_kernel<true, kMaxTopk>); });
+  else
+    by_topk(topk, [&] { go(moe_combine_backward_kernel<false, 4>); }, [&] { go(moe_combine_backward_kernel<false, 8>); },
+            [&] { go(moe_combine_backward_kernel<false, kMaxTopk>); });
+  if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
+  return FP8G_OK;
+}

@@ -1,0 +1,175 @@
+// moe_layout.cuh -- device code of the expert layouts: which row each routed
+// slot takes.  Routed row r = t * topk + k goes to expert e[r] (-1: dropped);
+// an expert's rows keep their order r.
+//
+// One cluster does the whole count -> scan -> rank chain: the slots are split
+// into one contiguous run per CTA and, inside it, one per warp.  A first walk
+// counts each warp's slots per expert (__match_any_sync finds the lanes of one
+// expert; the lowest adds their number to a counter that only its warp uses),
+// the warps' counters are scanned in shared memory and the CTAs' totals
+// through distributed shared memory, and a second walk hands out the rows.
+// Everything is integer work in a fixed order: ranks are stable.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fp8gemm.h"
+#include "ptx.cuh"
+
+namespace fp8g {
+namespace moe {
+
+constexpr int kMaxExperts = 256;
+constexpr int kMaxTopk = 16;
+constexpr int kLayoutThreads = 1024;
+constexpr int kLayoutWarps = kLayoutThreads / 32;
+
+// Expert of routed row r, or -1 (dropped, or out of range: flagged).
+__device__ __forceinline__ int expert_at(const int32_t* e, int G, long r, uint32_t* err) {
+  const int g = __ldg(e + r);
+  if (g < G && g >= -1) return g;
+  if (err) atomicOr(err, FP8G_DEVERR_BAD_EXPERT);
+  return -1;
+}
+
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// kMasked: pos[r] = g * Mmax + rank, -1 at and behind Mmax; counts[g] =
+// min(rows of g, Mmax).  Otherwise the contiguous layout: pos[r] = first row
+// of g's segment + rank, segments padded to 128 rows; counts = m_indices
+// [blocks].  Launched as one cluster of 1 to 8 CTAs.
+template <bool kMasked>
+__global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_t* __restrict__ expert, int R, int G,
+                                                                    int Mmax, int32_t* __restrict__ pos,
+                                                                    int32_t* __restrict__ counts, int blocks,
+                                                                    uint32_t* err) {
+  __shared__ int32_t s_w[kLayoutWarps][kMaxExperts];  // per warp: slots of each expert, then the warp's next rank
+  __shared__ int32_t s_total[kMaxExperts];            // this CTA's slots of each expert (read by the cluster)
+  __shared__ int32_t s_first[kMaxExperts];            // first row that this CTA hands out for each expert
+  __shared__ int32_t s_end[kMaxExperts];              // contiguous: end of each segment in blocks
+  __shared__ int32_t s_warp[kMaxExperts / 32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+  for (int i = tid; i < kLayoutWarps * kMaxExperts; i += kLayoutThreads) (&s_w[0][0])[i] = 0;
+  __syncthreads();
+  // rows of this warp: whole steps of 32 slots
+  const long steps = (static_cast<long>(R) + 32L * kLayoutWarps * ctas - 1) / (32L * kLayoutWarps * ctas);
+  const long r0 = (static_cast<long>(rank) * kLayoutWarps + w) * steps * 32;
+  for (long i = 0; i < steps; ++i) {
+    const long r = r0 + 32 * i + lane;
+    const int g = r < R ? expert_at(expert, G, r, err) : -1;
+    const uint32_t peers = __match_any_sync(0xffffffffu, g);
+    if (g >= 0 && (peers & ((1u << lane) - 1u)) == 0) s_w[w][g] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  if (tid < kMaxExperts) {
+    int32_t run = 0;
+#pragma unroll 8
+    for (int ww = 0; ww < kLayoutWarps; ++ww) {
+      const int32_t v = s_w[ww][tid];
+      s_w[ww][tid] = run;
+      run += v;
+    }
+    s_total[tid] = run;
+  }
+  cluster_sync_all();
+  int32_t before = 0, total = 0;
+  if (tid < kMaxExperts) {
+    const uint32_t mine = smem_u32(&s_total[tid]);
+    for (int c = 0; c < ctas; ++c) {
+      const int32_t v = ld_cluster_s32(mapa(mine, c));
+      if (c < rank) before += v;
+      total += v;
+    }
+  }
+  if constexpr (kMasked) {
+    if (tid < kMaxExperts) s_first[tid] = before;
+    if (rank == 0 && tid < G) {
+      counts[tid] = min(total, Mmax);
+      if (total > Mmax) atomicOr(err, FP8G_DEVERR_MASKED_OVER);
+    }
+    __syncthreads();
+  } else {
+    // inclusive scan of the segments' blocks over the experts (8 warps)
+    const int32_t nblk = (total + 127) / 128;
+    int32_t incl = nblk;
+    if (tid < kMaxExperts) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (lane == 31) s_warp[w] = incl;
+    }
+    __syncthreads();
+    if (tid < kMaxExperts) {
+      for (int i = 0; i < w; ++i) incl += s_warp[i];
+      s_end[tid] = incl;
+      s_first[tid] = (incl - nblk) * 128 + before;
+    }
+    __syncthreads();
+    for (int b = rank * kLayoutThreads + tid; b < blocks; b += ctas * kLayoutThreads) {
+      // the first expert whose segment ends behind block b
+      int lo = 0, hi = G;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (s_end[mid] > b) hi = mid;
+        else lo = mid + 1;
+      }
+      counts[b] = lo < G ? lo : -1;
+    }
+  }
+  for (long i = 0; i < steps; ++i) {
+    const long r = r0 + 32 * i + lane;
+    const int g = r < R ? expert_at(expert, G, r, nullptr) : -1;
+    const uint32_t peers = __match_any_sync(0xffffffffu, g);
+    const uint32_t below = peers & ((1u << lane) - 1u);
+    int32_t row = -1;
+    if (g >= 0) {
+      row = s_first[g] + s_w[w][g] + __popc(below);
+      if constexpr (kMasked) row = row < Mmax ? g * Mmax + row : -1;
+    }
+    __syncwarp();
+    if (g >= 0 && below == 0) s_w[w][g] += __popc(peers);
+    __syncwarp();
+    if (r < R) pos[r] = row;
+  }
+  // no CTA leaves while another may still read its totals
+  cluster_sync_all();
+}
+
+// One cluster of up to 8 CTAs, a CTA for every 4096 slots.
+template <bool kMasked>
+cudaError_t launch_layout(const int32_t* expert, int R, int G, int Mmax, int32_t* pos, int32_t* counts, int blocks,
+                          uint32_t* err, cudaStream_t stream) {
+  int ctas = 1;
+  while (ctas < 8 && R > 4096 * ctas) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kLayoutThreads, 1, 1);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_layout_kernel<kMasked>, expert, R, G, Mmax, pos, counts, blocks, err);
+}
+
+}  // namespace moe
+}  // namespace fp8g

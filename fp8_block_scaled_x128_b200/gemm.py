@@ -7,6 +7,7 @@ the shared library is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -19,7 +20,7 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is missing: build it with `python -m fp8_block_scaled_x128_b200.build` "
         "(the library has no CPU fallback)")
 
-_P, _I, _U32 = C.c_void_p, C.c_int, C.c_uint32
+_P, _I, _U32, _F = C.c_void_p, C.c_int, C.c_uint32, C.c_float
 
 lib = C.CDLL(LIB_PATH)
 lib.fp8_gemm_nt.restype = _I
@@ -44,6 +45,21 @@ lib.fp8g_moe_dispatch.restype = _I
 lib.fp8g_moe_dispatch.argtypes = [_P, _I, _I, _I, _P, _I, _I, _I, _P, _P, _I, _P, _P, _P, C.c_size_t, _P]
 lib.fp8g_moe_combine.restype = _I
 lib.fp8g_moe_combine.argtypes = [_P, _I, _P, _P, _I, _I, _P, _P]
+lib.fp8g_moe_dispatch_masked.restype = _I
+lib.fp8g_moe_dispatch_masked.argtypes = [_P, _I, _I, _I, _P, _I, _I, _I, _P, _P, _I, _P, _P, _P]
+lib.fp8g_moe_permute.restype = _I
+lib.fp8g_moe_permute.argtypes = [_P, _I, _I, _I, _P, _I, _I, _I, _P, _P, _P, _P]
+lib.fp8g_moe_permute_backward.restype = _I
+lib.fp8g_moe_permute_backward.argtypes = [_P, _I, _I, _I, _P, _I, _I, _P, _P]
+lib.fp8g_moe_combine_backward.restype = _I
+lib.fp8g_moe_combine_backward.argtypes = [_P, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P]
+lib.fp8g_norm_residual.restype = _I
+lib.fp8g_norm_residual.argtypes = [_P, _P, _I, _I, _I, _P, _P, _I, _F, _P, _F, _P, _P, _P, _P, _I, _P]
+lib.fp8g_norm_residual_backward_workspace_bytes.restype = C.c_size_t
+lib.fp8g_norm_residual_backward_workspace_bytes.argtypes = [_I, _I]
+lib.fp8g_norm_residual_backward.restype = _I
+lib.fp8g_norm_residual_backward.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _F, _P, _F, _P, _P, _P, _P, _P, _P,
+                                            C.c_size_t, _P]
 lib.bf16_gemm_nt.restype = _I
 lib.bf16_gemm_nt.argtypes = [_P, _P, _P, _I, _I, _I, _P]
 lib.fp8_gemm_nt_ue8m0.restype = _I
@@ -64,6 +80,7 @@ lib.fp8g_version.restype = _I
 lib.fp8g_version.argtypes = []
 
 DEVERR_TIMEOUT, DEVERR_BAD_M_INDEX, DEVERR_MASKED_OVER, DEVERR_BAD_EXPERT = 0x1, 0x2, 0x4, 0x8
+DEVERR_BAD_POS = 0x10
 
 
 class Fp8GemmError(RuntimeError):
@@ -326,6 +343,269 @@ def moe_combine(D, pos, w, T, topk, out=None, stream=None):
     with torch.cuda.device(dev):
         _check(lib.fp8g_moe_combine(_ptr(D), N, _ptr(pos), _ptr(w), int(T), int(topk), _ptr(out),
                                     _stream(stream, dev)), "fp8g_moe_combine")
+    return out
+
+
+def _shaped(t, dt, shape, name):
+    """t, if it is a contiguous CUDA tensor of this type and shape."""
+    if not t.is_cuda or t.dtype != dt or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise TypeError(f"{name}: expected a contiguous CUDA tensor of {dt} {tuple(shape)}, got {t.dtype} "
+                        f"{tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _rows(t, name):
+    if not t.is_cuda or t.dtype not in _IN_DTYPE or not t.is_contiguous() or t.dim() != 2:
+        raise TypeError(f"{name}: expected a contiguous 2-D CUDA tensor of bfloat16 or float32, got {t.dtype} "
+                        f"{tuple(t.shape)} on {t.device}")
+    return t
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """Runs a call under its operands' device and, if a stream is given, under
+    that stream, so that what the call allocates belongs to the stream it runs
+    on.  Gives the raw stream."""
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            yield torch.cuda.current_stream(dev).cuda_stream
+        else:
+            with torch.cuda.device(dev):
+                yield torch.cuda.current_stream(dev).cuda_stream
+        return
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the operands on {dev}")
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _tensors(**tensors):
+    return {name: t for name, t in tensors.items() if t is not None}
+
+
+def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
+    """Expert dispatch before the masked GEMM: x [T, K] (bfloat16 or float32),
+    expert [T*topk] int32 (-1 = dropped) -> (A [G, Mmax, K] uint8, sa [G, K/128,
+    ld_sa] float32, pos [T*topk] int32, masked_m [G] int32).  pos is the slot's
+    row of D seen as [G*Mmax, N], for moe_combine; slots past an expert's Mmax
+    rows are dropped and flagged (DEVERR_MASKED_OVER).  Rows behind masked_m
+    are not written.  `out` may pass those four tensors to reuse them."""
+    _rows(x, "x")
+    T, K = x.shape
+    topk, G, Mmax = int(topk), int(G), int(Mmax)
+    R = T * topk
+    _shaped(expert, torch.int32, (R,), "expert")
+    dev = _one_device(x=x, expert=expert)
+    with _on(dev, stream) as raw:
+        if out is None:
+            ld = (Mmax + 3) // 4 * 4
+            out = (torch.empty((G, Mmax, K), dtype=torch.uint8, device=dev),
+                   torch.empty((G, K // 128, ld), dtype=torch.float32, device=dev),
+                   torch.empty(R, dtype=torch.int32, device=dev), torch.empty(G, dtype=torch.int32, device=dev))
+        A, sa, pos, masked_m = out
+        _shaped(A, torch.uint8, (G, Mmax, K), "A")
+        _shaped(sa, torch.float32, (G, K // 128, sa.shape[-1]), "sa")
+        _shaped(pos, torch.int32, (R,), "pos"), _shaped(masked_m, torch.int32, (G,), "masked_m")
+        _one_device(x=x, A=A, sa=sa, pos=pos, masked_m=masked_m)
+        _check(lib.fp8g_moe_dispatch_masked(x.data_ptr(), _IN_DTYPE[x.dtype], T, K, expert.data_ptr(), topk, G, Mmax,
+                                            A.data_ptr(), sa.data_ptr(), sa.shape[-1], pos.data_ptr(),
+                                            masked_m.data_ptr(), raw), "fp8g_moe_dispatch_masked")
+    return A, sa, pos, masked_m
+
+
+def moe_permute(x, expert, topk, G, blocks=None, out=None, stream=None):
+    """Expert sort without quantisation, in moe_dispatch's contiguous layout: x
+    [T, N] (bfloat16 or float32), expert [T*topk] int32 (-1 = dropped) -> (xs
+    [blocks*128, N] of x's type, pos [T*topk] int32, m_indices [blocks] int32).
+    Padding rows of a segment are zero; unused blocks are not written.  `out`
+    may pass those three tensors to reuse them."""
+    _rows(x, "x")
+    T, N = x.shape
+    topk, G = int(topk), int(G)
+    R = T * topk
+    _shaped(expert, torch.int32, (R,), "expert")
+    nb = moe_blocks(T, topk, G) if blocks is None else int(blocks)
+    dev = _one_device(x=x, expert=expert)
+    with _on(dev, stream) as raw:
+        if out is None:
+            out = (torch.empty((nb * 128, N), dtype=x.dtype, device=dev),
+                   torch.empty(R, dtype=torch.int32, device=dev), torch.empty(nb, dtype=torch.int32, device=dev))
+        xs, pos, mi = out
+        _shaped(xs, x.dtype, (nb * 128, N), "xs")
+        _shaped(pos, torch.int32, (R,), "pos"), _shaped(mi, torch.int32, (nb,), "m_indices")
+        _one_device(x=x, xs=xs, pos=pos, m_indices=mi)
+        _check(lib.fp8g_moe_permute(x.data_ptr(), _IN_DTYPE[x.dtype], T, N, expert.data_ptr(), topk, G, nb,
+                                    xs.data_ptr(), pos.data_ptr(), mi.data_ptr(), raw), "fp8g_moe_permute")
+    return xs, pos, mi
+
+
+def moe_permute_backward(dxs, pos, T, topk, out=None, stream=None):
+    """Gradient of moe_permute (and of moe_dispatch, its quantisation taken as
+    the identity): dx [T, N] = sum over a token's slots of dxs[pos] (FP32 in
+    slot order, rounded once).  dxs [blocks*128, N] bfloat16 or float32."""
+    _rows(dxs, "dxs")
+    M, N = dxs.shape
+    T, topk = int(T), int(topk)
+    _layout_rows(M, "dxs")
+    _shaped(pos, torch.int32, (T * topk,), "pos")
+    dev = _one_device(dxs=dxs, pos=pos)
+    with _on(dev, stream) as raw:
+        dx = torch.empty((T, N), dtype=dxs.dtype, device=dev) if out is None else out
+        _shaped(dx, dxs.dtype, (T, N), "out")
+        _one_device(dxs=dxs, out=dx)
+        _check(lib.fp8g_moe_permute_backward(dxs.data_ptr(), _IN_DTYPE[dxs.dtype], M // 128, N, pos.data_ptr(), T,
+                                             topk, dx.data_ptr(), raw), "fp8g_moe_permute_backward")
+    return dx
+
+
+def _layout_rows(M, name):
+    if M % 128 != 0:
+        raise ValueError(f"{name}: {M} rows are not whole 128-row blocks")
+
+
+def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, stream=None):
+    """Gradient of moe_combine: dout [T, N], D [blocks*128, N] bfloat16, w
+    [T*topk] float32 or None -> (dD, dw), dD [blocks*128, N] bfloat16 with
+    dD[pos] = w * dout, dw [T*topk] float32 = <dout, D[pos]> (0 for dropped
+    slots; None if w is None).  quantize=True gives (q, sa, dw) instead: e4m3
+    codes and [N/128, ld_sa] scales, the A side of the grouped GEMM that
+    follows.  Unfilled rows of used blocks are zero, unused blocks are not
+    written.  `out` may pass the returned tensors to reuse them."""
+    T, topk = int(T), int(topk)
+    _dev(D, torch.bfloat16, "D")
+    M, N = D.shape
+    _layout_rows(M, "D")
+    _shaped(dout, torch.bfloat16, (T, N), "dout"), _shaped(pos, torch.int32, (T * topk,), "pos")
+    if w is not None:
+        _shaped(w, torch.float32, (T * topk,), "w")
+    dev = _one_device(**_tensors(dout=dout, D=D, pos=pos, w=w))
+    with _on(dev, stream) as raw:
+        if out is None:
+            dw = None if w is None else torch.empty(T * topk, dtype=torch.float32, device=dev)
+            if quantize:
+                out = (torch.empty((M, N), dtype=torch.uint8, device=dev),
+                       torch.empty((N // 128, max(M, 4)), dtype=torch.float32, device=dev), dw)
+            else:
+                out = (torch.empty((M, N), dtype=torch.bfloat16, device=dev), dw)
+        q = sa = dD = None
+        if quantize:
+            q, sa, dw = out
+            _shaped(q, torch.uint8, (M, N), "q"), _shaped(sa, torch.float32, (N // 128, sa.shape[-1]), "sa")
+        else:
+            dD, dw = out
+            _shaped(dD, torch.bfloat16, (M, N), "dD")
+        if (dw is None) != (w is None):
+            raise ValueError("dw: an output exactly if w is given")
+        if dw is not None:
+            _shaped(dw, torch.float32, (T * topk,), "dw")
+        _one_device(**_tensors(dout=dout, dD=dD, q=q, sa=sa, dw=dw))
+        _check(lib.fp8g_moe_combine_backward(dout.data_ptr(), D.data_ptr(), N, pos.data_ptr(), _addr(w), T, topk,
+                                             M // 128, _addr(dD), _addr(q), _addr(sa),
+                                             0 if sa is None else sa.shape[-1], _addr(dw), raw),
+               "fp8g_moe_combine_backward")
+    return out
+
+
+def _norm_params(y, post_weight, gate, pre_weight):
+    """Checks the parameters of rows y; the kind of the gate."""
+    rows, H = y.shape
+    for name, p in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if p is not None:
+            _shaped(p, torch.float32, (H,), name)
+    if gate is None:
+        return 0
+    if gate.dim() == 1:
+        _shaped(gate, torch.float32, (H,), "gate")
+        return 1
+    _shaped(gate, torch.float32, (rows, 1), "gate")
+    return 2
+
+
+def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=None, eps=1e-6, quantize=False, out=None,
+                  stream=None):
+    """The norms around a block with its gate, residual scale and residual sum:
+    h_out = h + scale * gate * post_weight * y / rms(y), z = pre_weight * h_out /
+    rms(h_out), rms(x) = sqrt(mean(x^2) + eps) -> (h_out, z), or (h_out, q, sa)
+    with quantize=True: z's e4m3 codes and [H/128, ld_sa] scales, the GEMM's
+    A-side inputs.  y, h [rows, H] bfloat16 or float32 (h None: no residual);
+    post_weight, pre_weight [H] float32 (post_weight None: no post-norm,
+    pre_weight None: ones); gate float32 [H] (per channel) or [rows, 1] (per
+    token).  `out` may pass the returned tensors; h_out may be h, z may be y."""
+    _rows(y, "y")
+    rows, H = y.shape
+    if h is not None:
+        _shaped(h, y.dtype, (rows, H), "h")
+    kind = _norm_params(y, post_weight, gate, pre_weight)
+    dev = _one_device(**_tensors(y=y, h=h, post_weight=post_weight, gate=gate, pre_weight=pre_weight))
+    with _on(dev, stream) as raw:
+        if out is None:
+            if quantize:
+                out = (torch.empty_like(y), torch.empty((rows, H), dtype=torch.uint8, device=dev),
+                       torch.zeros((max(1, H // 128), max(4, (rows + 3) // 4 * 4)), dtype=torch.float32, device=dev))
+            else:
+                out = (torch.empty_like(y), torch.empty_like(y))
+        z = q = sa = None
+        if quantize:
+            h_out, q, sa = out
+            _shaped(q, torch.uint8, (rows, H), "q"), _shaped(sa, torch.float32, (H // 128, sa.shape[-1]), "sa")
+        else:
+            h_out, z = out
+            _shaped(z, y.dtype, (rows, H), "z")
+        _shaped(h_out, y.dtype, (rows, H), "h_out")
+        _one_device(**_tensors(y=y, h_out=h_out, z=z, q=q, sa=sa))
+        _check(lib.fp8g_norm_residual(y.data_ptr(), _addr(h), _IN_DTYPE[y.dtype], rows, H, _addr(post_weight),
+                                      _addr(gate), kind, scale, _addr(pre_weight), eps, h_out.data_ptr(), _addr(z),
+                                      _addr(q), _addr(sa), 0 if sa is None else sa.shape[-1], raw),
+               "fp8g_norm_residual")
+    return out
+
+
+def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, scale=1.0, pre_weight=None, eps=1e-6,
+                           out=None, workspace=None, stream=None):
+    """Gradients of norm_residual from those of z and h_out (either may be None):
+    (dh, dy, dpre_weight, dpost_weight, dgate), the last three float32 in their
+    parameters' shapes, None where the parameter is None.  h_out and y are the
+    forward pass's.  `out` may pass the five tensors to reuse them (dh may be
+    dh_out), `workspace` float32 scratch of at least
+    fp8g_norm_residual_backward_workspace_bytes(rows, H) bytes."""
+    _rows(y, "y")
+    rows, H = y.shape
+    _shaped(h_out, y.dtype, (rows, H), "h_out")
+    for name, t in (("dz", dz), ("dh_out", dh_out)):
+        if t is not None:
+            _shaped(t, y.dtype, (rows, H), name)
+    kind = _norm_params(y, post_weight, gate, pre_weight)
+    dev = _one_device(**_tensors(y=y, h_out=h_out, dz=dz, dh_out=dh_out, post_weight=post_weight, gate=gate,
+                                 pre_weight=pre_weight))
+    with _on(dev, stream) as raw:
+        if out is None:
+            out = (torch.empty_like(y), torch.empty_like(y), *(None if p is None else torch.empty_like(p)
+                                                                for p in (pre_weight, post_weight, gate)))
+        dh, dy, dpre, dpost, dgate = out
+        _shaped(dh, y.dtype, (rows, H), "dh"), _shaped(dy, y.dtype, (rows, H), "dy")
+        for name, p, d in (("dpre_weight", pre_weight, dpre), ("dpost_weight", post_weight, dpost),
+                           ("dgate", gate, dgate)):
+            if (p is None) != (d is None):
+                raise ValueError(f"{name}: an output exactly if its parameter is given")
+            if d is not None:
+                _shaped(d, torch.float32, p.shape, name)
+        need = lib.fp8g_norm_residual_backward_workspace_bytes(rows, H)
+        if workspace is None and need:
+            workspace = torch.empty(need // 4, dtype=torch.float32, device=dev)
+        elif workspace is not None:
+            _dev(workspace, torch.float32, "workspace")
+        _one_device(**_tensors(y=y, dh=dh, dy=dy, dpre_weight=dpre, dpost_weight=dpost, dgate=dgate,
+                               workspace=workspace))
+        _check(lib.fp8g_norm_residual_backward(_addr(dz), _addr(dh_out), h_out.data_ptr(), y.data_ptr(),
+                                               _IN_DTYPE[y.dtype], rows, H, _addr(post_weight), _addr(gate), kind,
+                                               scale, _addr(pre_weight), eps, dh.data_ptr(), dy.data_ptr(), _addr(dpre),
+                                               _addr(dpost), _addr(dgate), _addr(workspace),
+                                               0 if workspace is None else workspace.numel() * 4, raw),
+               "fp8g_norm_residual_backward")
     return out
 
 

@@ -73,8 +73,9 @@ enum fp8g_status {
 /* Device-side error word bits (fp8g_get_device_error). */
 #define FP8G_DEVERR_TIMEOUT       0x1u  /* a pipeline wait gave up; outputs of that call are invalid */
 #define FP8G_DEVERR_BAD_M_INDEX   0x2u  /* contiguous: m_indices entry >= G (block skipped) */
-#define FP8G_DEVERR_MASKED_OVER   0x4u  /* masked: masked_m[g] > Mmax (clamped to Mmax) */
+#define FP8G_DEVERR_MASKED_OVER   0x4u  /* masked: masked_m[g] > Mmax, or more rows dispatched to g (clamped to Mmax) */
 #define FP8G_DEVERR_BAD_EXPERT    0x8u  /* MoE dispatch: an expert id >= G or < -1 (row dropped) */
+#define FP8G_DEVERR_BAD_POS       0x10u /* MoE gradients: a position outside the layout (slot skipped), or one row named by two slots */
 
 /*
  * Dense NT GEMM (GeekNews page, "일반 GEMM 성능 (Dense 모델)").
@@ -279,6 +280,144 @@ int fp8g_moe_dispatch(const void *x, int x_dtype, int T, int K,
  */
 int fp8g_moe_combine(const uint16_t *D, int N, const int32_t *pos, const float *w,
                      int T, int topk, uint16_t *out, cudaStream_t stream);
+
+/*
+ * Dispatch into the masked layout: the decode-time counterpart of
+ * fp8g_moe_dispatch, in front of m_grouped_fp8_gemm_nt_masked (GeekNews,
+ * "마스킹(masked) 레이아웃의 그룹화 GEMM").  Expert g's slots, in their order r,
+ * take rows 0, 1, ... of group g; token t is quantised per 1x128 group as by
+ * fp8g_quantize_1x128.
+ *   x [T][K] (bf16 patterns or FP32, x_dtype), K % 128 == 0, K <= 65536;
+ *   expert [T*topk] int32, -1 = dropped; 1 <= topk <= 16; 1 <= G <= 256;
+ *   outputs A [G][Mmax][K] e4m3 codes, sa [G][K/128][ld_sa] (ld_sa >= Mmax,
+ *   ld_sa % 4 == 0), masked_m [G] rows of each group, and pos [T*topk], the
+ *   slot's row g*Mmax + rank, or -1.  fp8g_moe_combine takes pos with the
+ *   GEMM's D seen as [G*Mmax][N].
+ * Slots of an expert past its Mmax-th are dropped (pos = -1, masked_m[g] =
+ * Mmax) and set FP8G_DEVERR_MASKED_OVER; an expert id out of range drops the
+ * slot and sets FP8G_DEVERR_BAD_EXPERT.  Rows at and behind masked_m[g] are
+ * left untouched.  T == 0 sets masked_m to zero.  One launch up to 4096
+ * routed slots, two above; no workspace.
+ * Errors: FP8G_ERR_INVALID_ARG (bad size, null pointer, G*Mmax above 2^31 -
+ * 1), FP8G_ERR_MISALIGNED (x, A, sa not 16-byte aligned; ld_sa), FP8G_ERR_CUDA.
+ */
+int fp8g_moe_dispatch_masked(const void *x, int x_dtype, int T, int K,
+                             const int32_t *expert, int topk, int G, int Mmax,
+                             uint8_t *A, float *sa, int ld_sa,
+                             int32_t *pos, int32_t *masked_m, cudaStream_t stream);
+
+/*
+ * Expert sort without quantisation: rows of x in the contiguous layout of
+ * fp8g_moe_dispatch (same pos, m_indices, segments and capacity), in x's type.
+ *   x [T][N] (bf16 patterns or FP32, x_dtype), N % 8 == 0, N >= 8;
+ *   xs [blocks*128][N]: xs[pos[r]] = x[r / topk]; padding rows of every
+ *   segment are zero, rows of unused blocks are not written.
+ * topk, G, blocks, expert, pos, m_indices and their errors as in
+ * fp8g_moe_dispatch.  No workspace.
+ */
+int fp8g_moe_permute(const void *x, int x_dtype, int T, int N,
+                     const int32_t *expert, int topk, int G, int blocks,
+                     void *xs, int32_t *pos, int32_t *m_indices, cudaStream_t stream);
+
+/*
+ * Gradients of the expert pipeline (mixture-of-experts training; the pages
+ * name training only as a use of the contiguous layout).  pos is the
+ * dispatch's or the permute's: each entry is -1 (dropped) or a row of the
+ * layout [blocks*128] that no other slot has.  An entry outside the layout
+ * is skipped and sets FP8G_DEVERR_BAD_POS; a row named twice sets the same
+ * flag (found by fp8g_moe_combine_backward, whose output it would leave
+ * undefined).  1 <= topk <= 16, N % 8 == 0, N >= 8.
+ *
+ * fp8g_moe_permute_backward: dx[t] = sum over k of dxs[pos[t*topk + k]], FP32
+ *   in slot order, rounded once; dropped slots add nothing.  It is the
+ *   gradient of fp8g_moe_permute, and of fp8g_moe_dispatch with the
+ *   quantisation taken as the identity.
+ *   dxs [blocks*128][N], dx [T][N], both of type `dtype`.
+ *
+ * fp8g_moe_combine_backward, for out[t] = sum over k of w[r] D[pos[r]]:
+ *     dD[pos[r]] = w[r] * dout[t]       (one FP32 product)
+ *     dw[r]      = sum over n of dout[t][n] * D[pos[r]][n]   (FP32; 0 if dropped)
+ *   dout [T][N], D [blocks*128][N] bf16 patterns; w [T*topk] or NULL (weights
+ *   of 1); dw [T*topk], or NULL to skip it (D is not read then).
+ *   The rows leave in one of two forms, the other's pointer being NULL:
+ *     dD [blocks*128][N] bf16 patterns, rounded once; or
+ *     q [blocks*128][N] e4m3 codes and sa [N/128][ld_sa] scales of the FP32
+ *     products, as fp8g_quantize_1x128 makes them: the A side of the grouped
+ *     GEMM that takes the gradient through the experts' weights
+ *     (N % 128 == 0, ld_sa >= blocks*128, ld_sa % 4 == 0).
+ *   The unfilled rows of every block that holds a routed row are set to zero
+ *   (codes and scales too); rows of unused blocks are not written.
+ * T == 0 is a no-op.  Errors: FP8G_ERR_INVALID_ARG, FP8G_ERR_MISALIGNED (rows
+ * not 16-byte aligned, N % 8, ld_sa % 4), FP8G_ERR_CUDA.
+ */
+int fp8g_moe_permute_backward(const void *dxs, int dtype, int blocks, int N,
+                              const int32_t *pos, int T, int topk, void *dx, cudaStream_t stream);
+
+int fp8g_moe_combine_backward(const uint16_t *dout, const uint16_t *D, int N,
+                              const int32_t *pos, const float *w, int T, int topk, int blocks,
+                              uint16_t *dD, uint8_t *q, float *sa, int ld_sa, float *dw,
+                              cudaStream_t stream);
+
+/*
+ * The norms before and after a block, with its gate, residual scale and
+ * residual sum, in one pass; z is the next block's input, ready for a GEMM:
+ *     u  = y / sqrt(mean(y^2) + eps)          (u = y if post_w is NULL)
+ *     h' = h + scale * g * post_w * u         (h = 0 if NULL, g = 1 without a gate)
+ *     z  = pre_w * h' / sqrt(mean(h'^2) + eps)  (pre_w = 1 if NULL)
+ * mean over the row's H values.  y is the block's output, h the residual
+ * stream.  All in FP32; h' and z are rounded once, z from the unrounded h'.
+ *   y, h, h_out [rows][H] of type `dtype` (FP8G_IN_BF16 or FP8G_IN_F32);
+ *   post_w, pre_w [H] FP32; gate [H] (FP8G_GATE_CHANNEL) or [rows]
+ *   (FP8G_GATE_TOKEN) FP32, NULL for FP8G_GATE_NONE;
+ *   either z [rows][H] of type `dtype`, or q [rows][H] e4m3 codes with sa
+ *   [H/128][ld_sa] scales (of the FP32 z, as fp8g_quantize_1x128 makes them;
+ *   H % 128 == 0, ld_sa >= rows, ld_sa % 4 == 0; entries past `rows` are not
+ *   written); the other's pointer is NULL.
+ * 8 <= H <= 16384, H % 8 == 0; eps > 0; scale finite.  h_out may be h's
+ * buffer and z may be y's; otherwise outputs overlap no input.
+ * rows == 0 is a no-op.  One launch, no workspace.
+ */
+#define FP8G_GATE_NONE 0
+#define FP8G_GATE_CHANNEL 1
+#define FP8G_GATE_TOKEN 2
+
+int fp8g_norm_residual(const void *y, const void *h, int dtype, int rows, int H,
+                       const float *post_w, const float *gate, int gate_kind, float scale,
+                       const float *pre_w, float eps,
+                       void *h_out, void *z, uint8_t *q, float *sa, int ld_sa, cudaStream_t stream);
+
+/*
+ * Gradients of fp8g_norm_residual.  dz and dh_out are the gradients of z and
+ * of h' (through the residual stream); either may be NULL (zero), not both.
+ * h_out and y are the forward pass's; its row statistics are recomputed from
+ * them.  With n = h' / sqrt(mean(h'^2) + eps), r1 and r2 the two factors
+ * 1 / sqrt(...), <.> the mean over the row:
+ *     dh     = dh_out + r1 * (dz pre_w - n <dz pre_w n>)
+ *     dy     = r2 * (du - u <du u>), du = scale * g * post_w * dh
+ *              (dy = du without a post-norm)
+ *     dpre_w = sum over rows of dz n
+ *     dpost_w = sum over rows of scale * g * dh u
+ *     dgate  = scale * post_w * dh u, summed over the rows ([H], per channel)
+ *              or over the row ([rows], per token)
+ *   dh, dy [rows][H] of type `dtype`; dpre_w, dpost_w [H], dgate FP32, each
+ *   NULL if it is not wanted (dpost_w needs post_w, dgate needs gate).
+ *   workspace: >= fp8g_norm_residual_backward_workspace_bytes(rows, H) bytes,
+ *   16-byte aligned, overwritten; needed for dpre_w, dpost_w and a channel
+ *   gate's dgate, otherwise it may be NULL.  Calls that may overlap on the GPU
+ *   need a workspace each.
+ * dh may be dh_out's buffer.  With rows == 0 the weights' gradients are set
+ * to zero.  Sums over rows run in a fixed order: the same call gives the same
+ * bits.  Errors of both: FP8G_ERR_INVALID_ARG, FP8G_ERR_MISALIGNED (rows and
+ * channel parameters not 16-byte aligned, H % 8, ld_sa % 4), FP8G_ERR_CUDA.
+ */
+size_t fp8g_norm_residual_backward_workspace_bytes(int rows, int H);
+
+int fp8g_norm_residual_backward(const void *dz, const void *dh_out, const void *h_out, const void *y,
+                                int dtype, int rows, int H,
+                                const float *post_w, const float *gate, int gate_kind, float scale,
+                                const float *pre_w, float eps,
+                                void *dh, void *dy, float *dpre_w, float *dpost_w, float *dgate,
+                                void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * BF16 NT GEMM on the same pipeline, the other input format the pages list
