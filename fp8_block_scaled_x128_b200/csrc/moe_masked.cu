@@ -33,6 +33,7 @@ using fp8g::moe::kMaxTopk;
 
 constexpr int kDirectSlots = 4096;
 constexpr int kThreads = 256;
+constexpr int kAhead = 8;  // loads of earlier slots in flight per lane
 
 // kDirect: ranks are counted here (grid T + 1, the last CTA counts rows per
 // expert); otherwise pos and masked_m are already there.
@@ -77,10 +78,20 @@ __global__ void __launch_bounds__(kThreads) moe_dispatch_masked_kernel(const voi
         n[k] = 0;
       }
       // earlier slots of each of this token's experts: a share per warp
-      for (long r = 32 * warp; r < t * topk; r += kThreads) {
-        const int g = r + lane < t * topk ? __ldg(expert + r + lane) : -1;
+      const int before = static_cast<int>(t) * topk;
+      for (int r0 = 32 * warp; r0 < before; r0 += kAhead * kThreads) {
+        int g[kAhead];
 #pragma unroll
-        for (int k = 0; k < kCap; ++k) n[k] += __popc(__ballot_sync(0xffffffffu, g == e[k]));
+        for (int i = 0; i < kAhead; ++i) {
+          const int r = r0 + i * kThreads + lane;
+          g[i] = r < before ? __ldg(expert + r) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (r0 + i * kThreads >= before) break;  // warp-uniform
+#pragma unroll
+          for (int k = 0; k < kCap; ++k) n[k] += __popc(__ballot_sync(0xffffffffu, g[i] == e[k]));
+        }
       }
       if (lane == 0) {
 #pragma unroll

@@ -79,30 +79,113 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// Sums of n values over the CTA, in every thread, in a fixed order (xor
-// butterflies: all lanes get the same bits).  One barrier per call: s holds two
-// buffers used in turn, and a buffer is written again only after the barrier
-// of the call in between, which every thread reaches after reading it.
-template <int n>
-struct BlockSum {
-  float s[2][n][32];
+// Four sums over a warp in 6 shuffles instead of 20: the first two steps halve
+// the values a lane carries, so the lanes of octet o end with the sum of v[o].
+__device__ __forceinline__ float warp_sum4(const float (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  const bool up = lane & 16, upper = lane & 8;
+  float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+  a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+  b += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+  float x = upper ? b : a;
+  x += __shfl_xor_sync(0xffffffffu, upper ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Sums of n (1 or 4) values over the kC CTAs of a cluster, in every thread, in
+// a fixed order that gives every thread the same bits.  One barrier per call:
+// s holds two buffers used in turn, and a buffer is written again only after
+// the barrier of the call in between, which every thread reaches after reading
+// it.  With kC > 1 every warp puts its sums into each CTA's shared memory, so
+// cluster_sync_all() has to come before the first call.
+template <int n, int kC>
+struct RowSum {
+  static_assert(n == 1 || n == 4, "one or four values");
+  float s[2][n][32 * kC];
 };
 
-template <int n>
-__device__ __forceinline__ void block_sum(float (&v)[n], BlockSum<n>& sm, int& turn) {
+template <int n, int kC>
+__device__ __forceinline__ void row_sum(float (&v)[n], RowSum<n, kC>& sm, int& turn, int rank) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  float mine;
+  if constexpr (n == 1) mine = warp_sum(v[0]);
+  else mine = warp_sum4(v);
+  if (kC > 1 || nw > 1) {
+    // the lanes that write: for each value and CTA of the cluster one
+    const int value = n == 1 ? 0 : lane >> 3, peer = n == 1 ? lane : lane & 7;
+    if constexpr (kC == 1) {
+      if (peer == 0) sm.s[turn][value][w] = mine;
+      __syncthreads();
+    } else {
+      if (peer < kC)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa(smem_u32(&sm.s[turn][value][32 * rank + w]), peer)),
+                     "f"(mine)
+                     : "memory");
+      cluster_sync_all();
+    }
+    if constexpr (n == 1) {
+      float x = 0.f;
 #pragma unroll
-  for (int i = 0; i < n; ++i) v[i] = warp_sum(v[i]);
-  const int nw = (blockDim.x + 31) >> 5;
-  if (nw == 1) return;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  if (lane == 0) {
+      for (int c = 0; c < kC; ++c) x += lane < nw ? sm.s[turn][0][32 * c + lane] : 0.f;
+      mine = warp_sum(x);
+    } else {
+      // octet o adds the warps' sums of value o
+      float x = 0.f;
 #pragma unroll
-    for (int i = 0; i < n; ++i) sm.s[turn][i][w] = v[i];
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x += peer + 8 * i < nw ? sm.s[turn][value][32 * c + peer + 8 * i] : 0.f;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      mine = x;
+    }
+    turn ^= 1;
   }
-  __syncthreads();
+  if constexpr (n == 1) {
+    v[0] = mine;
+  } else {
 #pragma unroll
-  for (int i = 0; i < n; ++i) v[i] = warp_sum(lane < nw ? sm.s[turn][i][lane] : 0.f);
-  turn ^= 1;
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, mine, 8 * i);
+  }
+}
+
+// ---------------------------------------------------------------- asynchronous copies
+// Each thread copies its own vectors of a row into shared memory and reads
+// back only those, so a finished copy needs no barrier, only cp_wait.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Until at most N committed groups of this thread are under way.
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 8 elements of a row, global to shared.
+template <bool kF32>
+__device__ __forceinline__ void copy8(uint32_t dst, const void* base, long e) {
+  const uint8_t* p = static_cast<const uint8_t*>(base) + e * (kF32 ? 4 : 2);
+  cp_async16(dst, p);
+  if constexpr (kF32) cp_async16(dst + 16, p + 16);
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+template <bool kF32>
+__device__ __forceinline__ Raw8<kF32> load8_shared(uint32_t addr) {
+  Raw8<kF32> r;
+  r.v[0] = ld_shared_v4(addr);
+  if constexpr (kF32) r.v[1] = ld_shared_v4(addr + 16);
+  return r;
 }
 
 // ---------------------------------------------------------------- host
