@@ -24,7 +24,7 @@
 
 #include "fp8gemm.h"
 #include "moe_layout.cuh"
-#include "quant_impl.cuh"
+#include "quant8.cuh"
 #include "rows.cuh"
 
 namespace {
@@ -98,10 +98,12 @@ __device__ __forceinline__ void pad_range(int cta, int pads, int blocks, int& b0
 }
 
 // ---------------------------------------------------------------- permute
-// CTAs [0, pads) zero padding rows; the others take a token each.  Rows are
-// moved as 16-byte vectors, whatever their type.
+// CTAs [0, pads) zero padding rows; the others take a part of a token's row
+// each, one 16-byte vector a thread, whatever the type: short CTAs leave little
+// work behind when the last ones run (with a CTA per token, 3.5 waves of 8 CTAs
+// an SM, the last wave ran half empty).
 template <int kCap>
-__global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int T, int topk,
+__global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int parts, int T, int topk,
                                                           const int32_t* __restrict__ pos, uint4* __restrict__ xs, int M,
                                                           int blocks, int pads, uint32_t* err) {
   __shared__ uint32_t bits[kPadBlocks * 4];
@@ -113,15 +115,15 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restric
     });
     return;
   }
-  for (long t = static_cast<long>(blockIdx.x) - pads; t < T; t += static_cast<long>(gridDim.x) - pads) {
-    int p[kCap];
+  const long items = static_cast<long>(T) * parts;
+  for (long i = static_cast<long>(blockIdx.x) - pads; i < items; i += static_cast<long>(gridDim.x) - pads) {
+    const long t = i / parts;
+    const int j = static_cast<int>(i - t * parts) * blockDim.x + threadIdx.x;
+    const uint4 v = j < vecs ? __ldcs(x + t * vecs + j) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int k = 0; k < kCap; ++k) p[k] = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
-    for (int j = threadIdx.x; j < vecs; j += blockDim.x) {
-      const uint4 v = __ldcs(x + t * vecs + j);
-#pragma unroll
-      for (int k = 0; k < kCap; ++k)
-        if (p[k] >= 0) __stcs(xs + static_cast<long>(p[k]) * vecs + j, v);
+    for (int k = 0; k < kCap; ++k) {
+      const int p = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+      if (p >= 0 && j < vecs) __stcs(xs + static_cast<long>(p) * vecs + j, v);
     }
   }
 }
@@ -155,20 +157,32 @@ __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* _
 }
 
 // ---------------------------------------------------------------- combine backward
-// kQuant: the rows leave as e4m3 codes and 1x128 scales (16 lanes hold a
-// group).  The group's largest |w x| is |w| times its largest |x|, rounded
-// once: rounding is monotonic, so one reduction over x serves every slot.
-template <bool kQuant, int kCap>
-__global__ void __launch_bounds__(256) moe_combine_backward_kernel(const uint16_t* __restrict__ dout,
-                                                                   const uint16_t* __restrict__ D, int N,
-                                                                   const int32_t* __restrict__ pos,
-                                                                   const float* __restrict__ w, int T, int topk,
-                                                                   uint16_t* __restrict__ dD, uint8_t* __restrict__ q,
-                                                                   float* __restrict__ sa, int ld_sa,
-                                                                   float* __restrict__ dw, int M, int blocks, int pads,
-                                                                   uint32_t* err) {
+// A CTA takes a token and walks its row in steps of blockDim vectors (8 columns
+// a thread); the slots of a step come in groups of kGroup.  A thread copies its
+// own vectors of the next (step, group) -- dout and each slot's D row -- into
+// shared memory (cp.async) before it works on the current one, so the loads of
+// kGroup + 1 rows are under way all the time without holding registers.
+//
+// kQuant: the rows leave as e4m3 codes and 1x128 scales; 16 lanes hold a group
+// of columns.  Its largest |w x| is |w| times its largest |x|, rounded once
+// (rounding is monotonic), so one reduction over x serves every slot; lane k of
+// the 16 forms slot k's scale and its reciprocal, and the others get them by
+// shuffle: the divisions are done once per group and slot, not in every lane.
+template <bool kQuant, int kGroup, int kGroups>
+__global__ void __launch_bounds__(256, 3) moe_combine_backward_kernel(const uint16_t* __restrict__ dout,
+                                                                      const uint16_t* __restrict__ D, int N,
+                                                                      const int32_t* __restrict__ pos,
+                                                                      const float* __restrict__ w, int T, int topk,
+                                                                      uint16_t* __restrict__ dD, uint8_t* __restrict__ q,
+                                                                      float* __restrict__ sa, int ld_sa,
+                                                                      float* __restrict__ dw, int M, int blocks, int pads,
+                                                                      uint32_t* err) {
+  constexpr int kSlots = kGroup * kGroups;
+  extern __shared__ __align__(16) uint8_t dyn[];  // two stages of kGroup + 1 vectors a thread
   __shared__ uint32_t bits[kPadBlocks * 4];
-  __shared__ float s_dot[8][kCap];
+  __shared__ float s_dot[8][kSlots];
+  __shared__ int s_pos[kSlots];
+  __shared__ float s_w[kSlots];
   if (static_cast<int>(blockIdx.x) < pads) {
     int b0, b1, slice;
     pad_range(blockIdx.x, pads, blocks, b0, b1, slice);
@@ -182,73 +196,114 @@ __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const uint16_
     return;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_row = N / 8;
+  const int own = lane & 15;  // the slot of a group whose scale this lane forms
+  const int per_row = N / 8, step = blockDim.x;
+  const int items = (per_row + step - 1) / step * kGroups;
+  const uint32_t pitch = step * 16, stage = (kGroup + 1) * pitch;
+  const uint32_t slot0 = fp8g::smem_u32(dyn) + threadIdx.x * 16;
   for (long t = static_cast<long>(blockIdx.x) - pads; t < T; t += static_cast<long>(gridDim.x) - pads) {
-    int p[kCap];
-    float wk[kCap], dot[kCap];
-#pragma unroll
-    for (int k = 0; k < kCap; ++k) {
-      p[k] = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
-      wk[k] = k < topk && w ? __ldg(w + t * topk + k) : 1.f;
-      dot[k] = 0.f;
+    if (threadIdx.x < kSlots) {
+      const int k = threadIdx.x;
+      s_pos[k] = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+      s_w[k] = k < topk && w ? __ldg(w + t * topk + k) : 1.f;
     }
-    // every thread of a warp takes part in the group maxima
-    for (int j0 = 0; j0 < per_row; j0 += blockDim.x) {
-      const int j = j0 + threadIdx.x;
-      const bool in = j < per_row;
-      const Raw8<false> raw = in ? load8<false>(dout, t * N + 8L * j) : zero8<false>();
-      Raw8<false> v[kCap];
-      if (dw) {
-#pragma unroll
-        for (int k = 0; k < kCap; ++k)
-          v[k] = in && p[k] >= 0 ? load8<false>(D, static_cast<long>(p[k]) * N + 8L * j) : zero8<false>();
-      }
-      float g[8];
-      unpack8<false>(raw, g);
-      float amax = 0.f;
-      if constexpr (kQuant) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(g[i]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      }
-#pragma unroll
-      for (int k = 0; k < kCap; ++k) {
-        if (p[k] < 0 || !in) continue;
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = wk[k] * g[i];
-        if constexpr (kQuant) {
-          const float sc = fp8g::quant::scale_of(fabsf(wk[k]) * amax);
-          uint32_t c[2];
-          fp8g::quant::encode_group(o, sc, c);
-          fp8g::quant::store_code_words(q + static_cast<long>(p[k]) * N + 8L * j, c);
-          if ((j & 15) == 0) sa[static_cast<long>(j >> 4) * ld_sa + p[k]] = sc;
-        } else {
-          store8<false>(dD, static_cast<long>(p[k]) * N + 8L * j, o);
-        }
+    __syncthreads();
+    auto fetch = [&](int i) {
+      const int j = i / kGroups * step + threadIdx.x;
+      if (i < items && j < per_row) {
+        const uint32_t at = slot0 + (i & 1) * stage;
+        cp_async16(at, dout + t * N + 8L * j);
         if (dw) {
-          float d[8];
-          unpack8<false>(v[k], d);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot[k] = fmaf(g[i], d[i], dot[k]);
+          for (int k = 0; k < kGroup; ++k) {
+            const int p = s_pos[i % kGroups * kGroup + k];
+            if (p >= 0) cp_async16(at + (k + 1) * pitch, D + static_cast<long>(p) * N + 8L * j);
+          }
+        }
+      }
+      cp_commit();
+    };
+    float dot[kSlots];
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) dot[k] = 0.f;
+    fetch(0);
+    for (int i0 = 0; i0 < items; i0 += kGroups) {
+#pragma unroll
+      for (int gi = 0; gi < kGroups; ++gi) {
+        const int i = i0 + gi;
+        fetch(i + 1);
+        cp_wait<1>();
+        const int j = i0 / kGroups * step + threadIdx.x;
+        const bool in = j < per_row;
+        const uint32_t at = slot0 + (i & 1) * stage;
+        float g[8];
+        unpack8<false>(in ? load8_shared<false>(at) : zero8<false>(), g);
+        Pair8 gp;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) gp.v[c] = pack2(g[2 * c], g[2 * c + 1]);
+        // every thread of a warp takes part in the groups' maxima and scales
+        float own_s = 1.f, own_y = 1.f;
+        bool tiny = false;
+        if constexpr (kQuant) {
+          float amax = 0.f;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(g[c]));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const int own_slot = gi * kGroup + (own < kGroup ? own : 0);
+          const int own_p = s_pos[own_slot];
+          amax *= fabsf(s_w[own_slot]);
+          tiny = __any_sync(0xffffffffu, amax > 0.f && amax < fp8g::quant::kTinyAmax);
+          own_s = tiny ? fp8g::quant::scale_of(amax) : fp8g::quant::normal_scale(amax);
+          own_y = __frcp_rn(own_s);
+          if (in && own < kGroup && own_p >= 0) sa[static_cast<long>(j >> 4) * ld_sa + own_p] = own_s;
+        }
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) {
+          const int p = s_pos[gi * kGroup + k];
+          if (p < 0) continue;  // the same for the whole CTA
+          const float wk = s_w[gi * kGroup + k];
+          if constexpr (kQuant) {
+            const float s = __shfl_sync(0xffffffffu, own_s, k, 16), y = __shfl_sync(0xffffffffu, own_y, k, 16);
+            uint32_t c[2];
+            if (tiny) {
+              float o[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = wk * g[e];
+              fp8g::quant::encode_group(o, s, c);
+            } else {
+              fp8g::quant::normal_codes_of_product(gp, wk, s, y, c);
+            }
+            if (in) fp8g::quant::store_code_words(q + static_cast<long>(p) * N + 8L * j, c);
+          } else if (in) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = wk * g[e];
+            store8<false>(dD, static_cast<long>(p) * N + 8L * j, o);
+          }
+          if (dw && in) {
+            const Pair8 d = pairs_of<false>(load8_shared<false>(at + (k + 1) * pitch));
+            uint64_t acc = mul2(gp.v[0], d.v[0]);
+#pragma unroll
+            for (int c = 1; c < 4; ++c) acc = fma2(gp.v[c], d.v[c], acc);
+            dot[gi * kGroup + k] += sum2(acc);
+          }
         }
       }
     }
     if (dw) {
 #pragma unroll
-      for (int k = 0; k < kCap; ++k) {
+      for (int k = 0; k < kSlots; ++k) {
         if (k >= topk) continue;
         const float sum = warp_sum(dot[k]);
         if (lane == 0) s_dot[warp][k] = sum;
       }
-      __syncthreads();
-      if (static_cast<int>(threadIdx.x) < topk) {
-        float sum = 0.f;
-        for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) sum += s_dot[i][threadIdx.x];
-        dw[t * topk + threadIdx.x] = sum;
-      }
-      __syncthreads();
+    }
+    __syncthreads();  // also: everyone has read s_pos and s_w
+    if (dw && static_cast<int>(threadIdx.x) < topk) {
+      float sum = 0.f;
+      for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) sum += s_dot[i][threadIdx.x];
+      dw[t * topk + threadIdx.x] = sum;
     }
   }
 }
@@ -267,7 +322,11 @@ void by_topk(int topk, F4 f4, F8 f8, F16 f16) {
   else f16();
 }
 
-int row_threads(long vecs) { return static_cast<int>(std::min<long>(256, std::max<long>(32, (vecs + 31) / 32 * 32))); }
+// Up to 256 threads that walk a row's vectors in equal steps.
+int row_threads(long vecs) {
+  const long steps = (vecs + 255) / 256;
+  return static_cast<int>(((vecs + steps - 1) / steps + 31) / 32 * 32);
+}
 
 int check_slots(int T, int topk, int N) {
   if (T < 0 || topk < 1 || topk > kMaxTopk || N < 1 || static_cast<long>(T) * topk > 0x7FFFFFFFL)
@@ -301,9 +360,10 @@ extern "C" int fp8g_moe_permute(const void* x, int x_dtype, int T, int N, const 
   const long vecs = static_cast<long>(N) * (x_dtype == FP8G_IN_F32 ? 4 : 2) / 16;
   if (vecs > 0x7FFFFFFFL) return FP8G_ERR_INVALID_ARG;
   const int pads = pad_ctas(blocks, sms);
-  const unsigned grid = static_cast<unsigned>(pads + std::min<long>(T, 32L * sms));
+  const int parts = static_cast<int>((vecs + 255) / 256);
+  const unsigned grid = static_cast<unsigned>(pads + std::min<long>(static_cast<long>(T) * parts, 1 << 20));
   auto go = [&](auto kernel) {
-    kernel<<<grid, row_threads(vecs), 0, stream>>>(static_cast<const uint4*>(x), static_cast<int>(vecs), T, topk, pos,
+    kernel<<<grid, row_threads(vecs), 0, stream>>>(static_cast<const uint4*>(x), static_cast<int>(vecs), parts, T, topk, pos,
                                                    static_cast<uint4*>(xs), blocks * 128, blocks, pads, err);
   };
   by_topk(topk, [&] { go(moe_permute_kernel<4>); }, [&] { go(moe_permute_kernel<8>); },
@@ -358,16 +418,25 @@ extern "C" int fp8g_moe_combine_backward(const uint16_t* dout, const uint16_t* D
   if (sms <= 0 || !err) return FP8G_ERR_CUDA;
   const int pads = pad_ctas(blocks, sms);
   const unsigned grid = static_cast<unsigned>(pads + std::min<long>(T, 32L * sms));
-  auto go = [&](auto kernel) {
-    kernel<<<grid, row_threads(N / 8), 0, stream>>>(dout, D, N, pos, w, T, topk, dD, q, sa, ld_sa, dw, blocks * 128,
-                                                    blocks, pads, err);
+  const int threads = row_threads(N / 8);
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto kernel, int group) {
+    const int smem = 2 * (group + 1) * threads * 16;  // at most 72 KB
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 72 << 10);
+    if (e == cudaSuccess)
+      kernel<<<grid, threads, smem, stream>>>(dout, D, N, pos, w, T, topk, dD, q, sa, ld_sa, dw, blocks * 128, blocks, pads,
+                                              err);
   };
   if (q)
-    by_topk(topk, [&] { go(moe_combine_backward_kernel<true, 4>); }, [&] { go(moe_combine_backward_kernel<true, 8>); },
-            [&] { go(moe_combine_backward_kernel<true, kMaxTopk>); });
+    by_topk(topk, [&] { go(moe_combine_backward_kernel<true, 4, 1>, 4); },
+            [&] { go(moe_combine_backward_kernel<true, 8, 1>, 8); }, [&] { go(moe_combine_backward_kernel<true, 8, 2>, 8); });
   else
-    by_topk(topk, [&] { go(moe_combine_backward_kernel<false, 4>); }, [&] { go(moe_combine_backward_kernel<false, 8>); },
-            [&] { go(moe_combine_backward_kernel<false, kMaxTopk>); });
+    by_topk(topk, [&] { go(moe_combine_backward_kernel<false, 4, 1>, 4); },
+            [&] { go(moe_combine_backward_kernel<false, 8, 1>, 8); }, [&] { go(moe_combine_backward_kernel<false, 8, 2>, 8); });
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FP8G_ERR_CUDA;
+  }
   if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
   return FP8G_OK;
 }

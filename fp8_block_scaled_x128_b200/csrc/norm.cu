@@ -29,7 +29,7 @@
 #include <cstdint>
 
 #include "fp8gemm.h"
-#include "quant_impl.cuh"
+#include "quant8.cuh"
 #include "rows.cuh"
 
 namespace {
@@ -37,7 +37,7 @@ namespace {
 using namespace fp8g::rows;
 using fp8g::cluster_ctarank;
 using fp8g::cluster_sync_all;
-using fp8g::smem_u32;
+using fp8g::quant::quantize8;
 
 constexpr int kMaxH = 16384;
 
@@ -54,7 +54,7 @@ __host__ __device__ constexpr int forward_stages(bool f32) { return f32 ? 3 : 4;
 struct Shape {
   int rows, H;
   int cols;      // columns of a CTA (the last of a cluster may have fewer)
-  uint32_t pitch;  // bytes of one row's part in shared memory
+  uint32_t pitch;  // bytes of one row's part in shared memory (whole warps of it)
 };
 
 struct Params {
@@ -64,17 +64,16 @@ struct Params {
 };
 
 // Parameters of columns col .. col + 7: pre_w, and a = post_w times a gate per channel.
-__device__ __forceinline__ void column_params(const Params& p, int col, bool in, float (&pw)[8], float (&a)[8]) {
+__device__ __forceinline__ void column_params(const Params& p, int col, bool in, Pair8& pre, Pair8& a) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) pw[i] = a[i] = 1.f;
+  for (int i = 0; i < 4; ++i) pre.v[i] = a.v[i] = both(1.f);
   if (!in) return;
-  if (p.pre_w) load_param8(p.pre_w, col, pw);
-  if (p.post_w) load_param8(p.post_w, col, a);
+  if (p.pre_w) pre = load_param8(p.pre_w, col);
+  if (p.post_w) a = load_param8(p.post_w, col);
   if (p.gate_kind == FP8G_GATE_CHANNEL) {
-    float g[8];
-    load_param8(p.gate, col, g);
+    const Pair8 g = load_param8(p.gate, col);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] *= g[i];
+    for (int i = 0; i < 4; ++i) a.v[i] = mul2(a.v[i], g.v[i]);
   }
 }
 
@@ -90,76 +89,157 @@ __device__ __forceinline__ float rms_factor(float sum, float inv_h, float eps) {
   return isinf(x) ? r : refined;
 }
 
+// The stages of a CTA: kTensors rows each, walked in step with its rows.  A
+// thread's slots of a tensor that is not there, and all slots of a thread
+// without columns, are zeroed once and never copied to, so the arithmetic needs
+// no conditions.  Addresses advance by additions only: with a multiplication
+// per row and tensor, a third of the instructions were address arithmetic.
+template <bool kF32, int kTensors, int kStages>
+struct Stream {
+  const uint8_t* src[kTensors];  // this thread's columns of the next row to fetch
+  uint32_t slot, stage_bytes, pitch;
+  uint32_t put, get_at;  // stages to fill and to read, as offsets
+  long step_bytes;       // bytes from a CTA's row to its next
+  long next;             // the next row to fetch
+  bool in, third, fourth;
+
+  static constexpr int kVec = kF32 ? 32 : 16;  // bytes of 8 elements
+
+  __device__ __forceinline__ void init(const void* const (&t)[kTensors], const uint8_t* smem, const Shape& S, int col0,
+                                       bool has_columns, long row0, long step) {
+    slot = fp8g::smem_u32(smem) + threadIdx.x * kVec;
+    pitch = S.pitch;
+    stage_bytes = kTensors * pitch;
+    put = get_at = 0;
+    in = has_columns;
+    next = row0;
+    const long row_bytes = static_cast<long>(S.H) * (kVec / 8);
+    step_bytes = step * row_bytes;
+#pragma unroll
+    for (int i = 0; i < kTensors; ++i) {
+      if (!in || !t[i]) {
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) {
+          st_shared_zero16(slot + s * stage_bytes + i * pitch);
+          if constexpr (kF32) st_shared_zero16(slot + s * stage_bytes + i * pitch + 16);
+        }
+      }
+      src[i] = static_cast<const uint8_t*>(t[i]) + (row0 * row_bytes + static_cast<long>(col0) * (kVec / 8) + threadIdx.x * kVec);
+    }
+    third = kTensors > 2 && t[kTensors > 2 ? 2 : 0];
+    fourth = kTensors > 3 && t[kTensors > 3 ? 3 : 0];
+    if (kTensors == 2) third = t[1] != nullptr;  // the forward pass's residual
+  }
+
+  // Copies this thread's part of the next row, if there is one, into the next stage.
+  __device__ __forceinline__ void fetch(int rows, long step) {
+    if (next < rows && in) {
+      const uint32_t at = slot + put;
+      copy8<kF32>(at, src[0]);
+      if constexpr (kTensors == 2) {
+        if (third) copy8<kF32>(at + pitch, src[1]);
+      } else {
+        copy8<kF32>(at + pitch, src[1]);
+        if (third) copy8<kF32>(at + 2 * pitch, src[2]);
+        if (fourth) copy8<kF32>(at + 3 * pitch, src[3]);
+      }
+    }
+    cp_commit();
+    next += step;
+#pragma unroll
+    for (int i = 0; i < kTensors; ++i) src[i] += step_bytes;
+    put = put == (kStages - 1) * stage_bytes ? 0 : put + stage_bytes;
+  }
+
+  __device__ __forceinline__ Pair8 get(int tensor) const {
+    return pairs_of<kF32>(load8_shared<kF32>(slot + get_at + tensor * pitch));
+  }
+
+  __device__ __forceinline__ void advance() { get_at = get_at == (kStages - 1) * stage_bytes ? 0 : get_at + stage_bytes; }
+};
+
+// Stores a thread's 8 values of a row, rounded once.
+template <bool kF32>
+__device__ __forceinline__ void put8(uint8_t* at, const Pair8& p) {
+  float f[8];
+  values_of(p, f);
+  store8<kF32>(at, 0, f);
+}
+
 template <bool kF32, int kC, bool kQuant>
 __global__ void __launch_bounds__(1024) norm_residual_kernel(const void* y, const void* h, Shape S, Params P, void* h_out,
                                                              void* z, uint8_t* q, float* sa, int ld_sa) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ RowSum<1, kC> sm;
   constexpr int D = forward_stages(kF32);
-  constexpr int kVec = kF32 ? 32 : 16;  // bytes of 8 elements
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
-  const int local = 8 * threadIdx.x;
-  const int col = rank * S.cols + local;
-  const bool in = local < S.cols && col < S.H;
-  const uint32_t slot = smem_u32(dyn) + threadIdx.x * kVec;  // stage s: y at slot + 2 s pitch, h behind it
-  auto fetch = [&](long row, int s) {
-    if (in && row < S.rows) {
-      copy8<kF32>(slot + 2 * s * S.pitch, y, row * S.H + col);
-      if (h) copy8<kF32>(slot + (2 * s + 1) * S.pitch, h, row * S.H + col);
-    }
-    cp_commit();
-  };
+  const int col0 = rank * S.cols, col = col0 + 8 * threadIdx.x;
+  const bool in = 8 * static_cast<int>(threadIdx.x) < S.cols && col < S.H;
+  Stream<kF32, 2, D> src;
+  src.init({y, h}, dyn, S, col0, in, row0, step);
 #pragma unroll
-  for (int s = 0; s < D - 1; ++s) fetch(row0 + s * step, s);
-  float pw[8], a[8];
+  for (int s = 0; s < D - 1; ++s) src.fetch(S.rows, step);
+  const long first = (row0 * S.H + col) * (src.kVec / 8);
+  uint8_t *h_at = static_cast<uint8_t*>(h_out) + first, *z_at = static_cast<uint8_t*>(z) + first;
+  uint8_t* q_at = q + (row0 * S.H + col);
+  float* sa_at = sa + (static_cast<long>(col / 128) * ld_sa + row0);
+  Pair8 pw, a;
   column_params(P, col, in, pw, a);
   if constexpr (kC > 1) cluster_sync_all();
   const float inv_h = 1.f / static_cast<float>(S.H);
-  int turn = 0, s = 0;
+  int turn = 0;
   for (long row = row0; row < S.rows; row += step) {
-    fetch(row + (D - 1) * step, s == 0 ? D - 1 : s - 1);
+    src.fetch(S.rows, step);
     cp_wait<D - 1>();
-    float hv[8], yv[8];
-    unpack8<kF32>(in ? load8_shared<kF32>(slot + 2 * s * S.pitch) : zero8<kF32>(), yv);
-    unpack8<kF32>(in && h ? load8_shared<kF32>(slot + (2 * s + 1) * S.pitch) : zero8<kF32>(), hv);
-    s = s == D - 1 ? 0 : s + 1;
+    const Pair8 yv = src.get(0);
+    Pair8 hv = src.get(1);
+    src.advance();
     float f = P.scale;
     if (P.gate_kind == FP8G_GATE_TOKEN) f *= __ldg(P.gate + row);
-    float ss[1] = {0.f};
+    float ss[1];
     if (P.post_w) {
+      uint64_t acc = mul2(yv.v[0], yv.v[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss[0] = fmaf(yv[i], yv[i], ss[0]);
+      for (int i = 1; i < 4; ++i) acc = fma2(yv.v[i], yv.v[i], acc);
+      ss[0] = sum2(acc);
       row_sum<1, kC>(ss, sm, turn, rank);
       f *= rms_factor(ss[0], inv_h, P.eps);
-      ss[0] = 0.f;
     }
+    uint64_t acc = 0;
+    const uint64_t ff = both(f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hv[i] = fmaf(a[i], yv[i] * f, hv[i]);
-      ss[0] = fmaf(hv[i], hv[i], ss[0]);
+    for (int i = 0; i < 4; ++i) {
+      hv.v[i] = fma2(a.v[i], mul2(yv.v[i], ff), hv.v[i]);
+      acc = fma2(hv.v[i], hv.v[i], acc);
     }
-    if (in) store8<kF32>(h_out, row * S.H + col, hv);
+    if (in) put8<kF32>(h_at, hv);
+    h_at += src.step_bytes;
+    ss[0] = sum2(acc);
     row_sum<1, kC>(ss, sm, turn, rank);
-    const float r1 = rms_factor(ss[0], inv_h, P.eps);
+    const uint64_t r1 = both(rms_factor(ss[0], inv_h, P.eps));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) hv[i] = pw[i] * (hv[i] * r1);
+    for (int i = 0; i < 4; ++i) hv.v[i] = mul2(pw.v[i], mul2(hv.v[i], r1));
     if constexpr (kQuant) {
       // 16 lanes hold a 1x128 group (a CTA's columns are whole groups: a half-warp is all in or all out)
-      float amax = 0.f;
+      float v[8], amax = 0.f;
+      values_of(hv, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(hv[i]));
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float sc = fp8g::quant::scale_of(amax);
+      float sc;
       uint32_t c[2];
-      fp8g::quant::encode_group(hv, sc, c);
+      quantize8(v, amax, sc, c);
       if (in) {
-        fp8g::quant::store_code_words(q + row * S.H + col, c);
-        if ((threadIdx.x & 15) == 0) sa[static_cast<long>(col / 128) * ld_sa + row] = sc;
+        fp8g::quant::store_code_words(q_at, c);
+        if ((threadIdx.x & 15) == 0) *sa_at = sc;
       }
+      q_at += step * S.H;
+      sa_at += step;
     } else {
-      if (in) store8<kF32>(z, row * S.H + col, hv);
+      if (in) put8<kF32>(z_at, hv);
+      z_at += src.step_bytes;
     }
   }
 }
@@ -176,101 +256,101 @@ __global__ void __launch_bounds__(kThreads) norm_residual_backward_kernel(const 
                                                                       const void* y, Shape S, Params P, void* dh, void* dy,
                                                                       float* __restrict__ dgate, float* __restrict__ part) {
   extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ RowSum<4, kC> sm3;
+  __shared__ RowSum<4, kC> sm4;
   __shared__ RowSum<1, kC> sm1;
   constexpr int D = kBackwardStages;
-  constexpr int kVec = kF32 ? 32 : 16;
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
-  const int local = 8 * threadIdx.x;
-  const int col = rank * S.cols + local;
-  const bool in = local < S.cols && col < S.H;
-  const uint32_t slot = smem_u32(dyn) + threadIdx.x * kVec;  // a stage: h, y, dz, dh_out
-  auto fetch = [&](long row, int s) {
-    if (in && row < S.rows) {
-      const uint32_t at = slot + 4 * s * S.pitch;
-      const long e = row * S.H + col;
-      copy8<kF32>(at, h, e);
-      copy8<kF32>(at + S.pitch, y, e);
-      if (dz) copy8<kF32>(at + 2 * S.pitch, dz, e);
-      if (dh_out) copy8<kF32>(at + 3 * S.pitch, dh_out, e);
-    }
-    cp_commit();
-  };
+  const int col0 = rank * S.cols, col = col0 + 8 * threadIdx.x;
+  const bool in = 8 * static_cast<int>(threadIdx.x) < S.cols && col < S.H;
+  Stream<kF32, 4, D> src;
+  src.init({h, y, dz, dh_out}, dyn, S, col0, in, row0, step);
 #pragma unroll
-  for (int s = 0; s < D - 1; ++s) fetch(row0 + s * step, s);
-  float pw[8], a[8];
-  column_params(P, col, in, pw, a);
+  for (int s = 0; s < D - 1; ++s) src.fetch(S.rows, step);
+  const long first = (row0 * S.H + col) * (src.kVec / 8);
+  uint8_t *dh_at = static_cast<uint8_t*>(dh) + first, *dy_at = static_cast<uint8_t*>(dy) + first;
+  Pair8 pw;
+  // s post_w (g per channel), used once a row: kept in shared memory, which
+  // leaves the registers to what every phase needs
+  const uint32_t a_at = src.slot - threadIdx.x * src.kVec + D * src.stage_bytes + threadIdx.x * 32;
+  {
+    Pair8 a;
+    column_params(P, col, in, pw, a);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] *= P.scale;
+    for (int i = 0; i < 4; ++i) a.v[i] = mul2(a.v[i], both(P.scale));
+    float v[8];
+    values_of(a, v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      fp8g::st_shared_v4(a_at + 16 * i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+  }
   if constexpr (kC > 1) cluster_sync_all();
   const float inv_h = 1.f / static_cast<float>(S.H);
-  float acc_pre[8] = {}, acc_u[8] = {};
-  int turn3 = 0, turn1 = 0, s = 0;
+  const bool token = P.gate_kind == FP8G_GATE_TOKEN;
+  Pair8 acc_pre = {}, acc_u = {};
+  int turn4 = 0, turn1 = 0;
   for (long row = row0; row < S.rows; row += step) {
-    fetch(row + (D - 1) * step, s == 0 ? D - 1 : s - 1);
+    src.fetch(S.rows, step);
     cp_wait<D - 1>();
-    const uint32_t at = slot + 4 * s * S.pitch;
-    s = s == D - 1 ? 0 : s + 1;
-    float st[4] = {0.f, 0.f, 0.f, 0.f};  // h'^2, (dz pre_w) h', y^2
-    float hv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, dhv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    float yv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in) {
-      unpack8<kF32>(load8_shared<kF32>(at), hv);
-      unpack8<kF32>(load8_shared<kF32>(at + S.pitch), yv);
-      if (dz) unpack8<kF32>(load8_shared<kF32>(at + 2 * S.pitch), dhv);
+    const Pair8 hv = src.get(0);
+    Pair8 yv = src.get(1), g = src.get(2);  // g: dz, then dh, then du
+    uint64_t hh = 0, dn = 0, yy = 0;              // h'^2, (dz pre_w) h', y^2
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        st[0] = fmaf(hv[i], hv[i], st[0]);
-        st[1] = fmaf(dhv[i] * pw[i], hv[i], st[1]);
-        st[2] = fmaf(yv[i], yv[i], st[2]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      hh = fma2(hv.v[i], hv.v[i], hh);
+      dn = fma2(mul2(g.v[i], pw.v[i]), hv.v[i], dn);
+      yy = fma2(yv.v[i], yv.v[i], yy);
     }
-    row_sum<4, kC>(st, sm3, turn3, rank);
+    float st[4] = {sum2(hh), sum2(dn), sum2(yy), 0.f};
+    row_sum<4, kC>(st, sm4, turn4, rank);
     const float r1 = rms_factor(st[0], inv_h, P.eps);
     const float r2 = P.post_w ? rms_factor(st[2], inv_h, P.eps) : 1.f;
-    const float m1 = st[1] * r1 * inv_h;  // <dz pre_w n>
-    const float gt = P.gate_kind == FP8G_GATE_TOKEN ? __ldg(P.gate + row) : 1.f;
-    float dot[1] = {0.f};  // sum of s a dh u
-    if (in) {
-      float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (dh_out) unpack8<kF32>(load8_shared<kF32>(at + 3 * S.pitch), t);
-      const float rm = -r1 * m1;
+    const float gt = token ? __ldg(P.gate + row) : 1.f;
+    const Pair8 t = src.get(3);
+    src.advance();
+    const uint64_t rr1 = both(r1), rr2 = both(r2);
+    const uint64_t rm = both(-r1 * (st[1] * r1 * inv_h));  // - r1 <dz pre_w n>
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float n = hv[i] * r1;
-        acc_pre[i] = fmaf(dhv[i], n, acc_pre[i]);
-        dhv[i] = fmaf(n, rm, fmaf(dhv[i] * pw[i], r1, t[i]));
-      }
-      store8<kF32>(dh, row * S.H + col, dhv);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t n = mul2(hv.v[i], rr1);
+      acc_pre.v[i] = fma2(g.v[i], n, acc_pre.v[i]);
+      g.v[i] = fma2(n, rm, fma2(mul2(g.v[i], pw.v[i]), rr1, t.v[i]));
+    }
+    if (in) put8<kF32>(dh_at, g);
+    dh_at += src.step_bytes;
+    const Pair8 a = pairs_of<true>(load8_shared<true>(a_at));
+    uint64_t du_u = 0;  // a dh u
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        yv[i] *= r2;
-        acc_u[i] = fmaf(gt * dhv[i], yv[i], acc_u[i]);
-        dhv[i] *= a[i];
-        dot[0] = fmaf(dhv[i], yv[i], dot[0]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      yv.v[i] = mul2(yv.v[i], rr2);
+      acc_u.v[i] = fma2(token ? mul2(g.v[i], both(gt)) : g.v[i], yv.v[i], acc_u.v[i]);
+      g.v[i] = mul2(g.v[i], a.v[i]);
+      du_u = fma2(g.v[i], yv.v[i], du_u);
     }
     float m2 = 0.f;  // <du u>
-    if (P.post_w || P.gate_kind == FP8G_GATE_TOKEN) {
+    if (P.post_w || token) {
+      float dot[1] = {sum2(du_u)};
       row_sum<1, kC>(dot, sm1, turn1, rank);
       if (P.post_w) m2 = dot[0] * gt * inv_h;
-      if (dgate && P.gate_kind == FP8G_GATE_TOKEN && rank == 0 && threadIdx.x == 0) dgate[row] = dot[0];
+      if (dgate && token && rank == 0 && threadIdx.x == 0) dgate[row] = dot[0];
     }
-    if (in) {
+    const uint64_t f = both(r2 * gt), um = both(-r2 * m2);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dhv[i] = r2 * fmaf(dhv[i], gt, -yv[i] * m2);
-      store8<kF32>(dy, row * S.H + col, dhv);
-    }
+    for (int i = 0; i < 4; ++i) g.v[i] = fma2(g.v[i], f, mul2(yv.v[i], um));
+    if (in) put8<kF32>(dy_at, g);
+    dy_at += src.step_bytes;
   }
   if (part && in) {
     float* p = part + row0 * S.H + col;
     float* pu = p + step * S.H;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      reinterpret_cast<float4*>(p)[i] = make_float4(acc_pre[4 * i], acc_pre[4 * i + 1], acc_pre[4 * i + 2], acc_pre[4 * i + 3]);
-      reinterpret_cast<float4*>(pu)[i] = make_float4(acc_u[4 * i], acc_u[4 * i + 1], acc_u[4 * i + 2], acc_u[4 * i + 3]);
-    }
+    float v[8];
+    values_of(acc_pre, v);
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    values_of(acc_u, v);
+    reinterpret_cast<float4*>(pu)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(pu)[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
 }
 
@@ -326,18 +406,18 @@ struct Plan {
 };
 
 constexpr int kSms = 148;
-constexpr int kSmemPerSm = 220 << 10;
+constexpr int kSmemPerSm = 225 << 10;
 
 // tensors: rows streamed per stage.  The cluster grows until a CTA has at most
 // 1024 threads and its stages fit the shared memory; narrow rows get as many
 // CTAs per SM as 72 registers a thread and their stages allow.
-Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit) {
+Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int more_per_thread) {
   Plan p{};
   for (p.ctas = 1;; p.ctas *= 2) {
     const int units = (H / unit + p.ctas - 1) / p.ctas;
-    p.S = Shape{rows, H, units * unit, static_cast<uint32_t>(units * unit * esz)};
-    p.threads = (p.S.cols / 8 + 31) / 32 * 32;
-    p.smem = tensors * stages * static_cast<int>(p.S.pitch);
+    p.threads = (units * unit / 8 + 31) / 32 * 32;
+    p.S = Shape{rows, H, units * unit, static_cast<uint32_t>(p.threads * 8 * esz)};
+    p.smem = tensors * stages * static_cast<int>(p.S.pitch) + more_per_thread * p.threads;
     if (p.ctas == 4 || (p.threads <= 1024 && p.smem <= kSmemPerSm)) break;
   }
   const int per_sm = std::max(1, std::min({32, 896 / p.threads, kSmemPerSm / (p.smem + 1024)}));
@@ -349,11 +429,11 @@ Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit) {
 // same order whether it leaves as values or as codes, in either type (1 CTA up
 // to H = 8192, 2 above).
 Plan forward_plan(int rows, int H, int dtype) {
-  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 2, forward_stages(dtype == FP8G_IN_F32), H % 128 == 0 ? 128 : 8);
+  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 2, forward_stages(dtype == FP8G_IN_F32), H % 128 == 0 ? 128 : 8, 0);
 }
 
 Plan backward_plan(int rows, int H, int dtype) {
-  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 4, kBackwardStages, 8);
+  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 4, kBackwardStages, 8, 32);
 }
 
 // Launches the kernel for the plan's cluster size.

@@ -67,10 +67,62 @@ __device__ __forceinline__ void store8(void* base, long e, const float (&f)[8]) 
   }
 }
 
+// 8 FP32 values as four packed pairs: one FP32x2 instruction (sm_100) does the
+// work of two, with the same rounding, which matters where the kernels are
+// bound by instructions issued rather than by the FP32 pipe.
+struct Pair8 {
+  uint64_t v[4];
+};
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ void split2(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t both(float x) { return pack2(x, x); }
+
+__device__ __forceinline__ float sum2(uint64_t p) {
+  float lo, hi;
+  split2(p, lo, hi);
+  return lo + hi;
+}
+
+template <bool kF32>
+__device__ __forceinline__ Pair8 pairs_of(const Raw8<kF32>& r) {
+  float f[8];
+  unpack8<kF32>(r, f);
+  Pair8 p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p.v[i] = pack2(f[2 * i], f[2 * i + 1]);
+  return p;
+}
+
+__device__ __forceinline__ void values_of(const Pair8& p, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2(p.v[i], f[2 * i], f[2 * i + 1]);
+}
+
 // 8 FP32 parameters (16-byte aligned), kept in cache: every row uses them.
-__device__ __forceinline__ void load_param8(const float* p, long e, float (&f)[8]) {
+__device__ __forceinline__ Pair8 load_param8(const float* p, long e) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p + e)), b = __ldg(reinterpret_cast<const float4*>(p + e) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  return Pair8{pack2(a.x, a.y), pack2(a.z, a.w), pack2(b.x, b.y), pack2(b.z, b.w)};
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -168,11 +220,12 @@ __device__ __forceinline__ void cp_wait() {
 
 // 8 elements of a row, global to shared.
 template <bool kF32>
-__device__ __forceinline__ void copy8(uint32_t dst, const void* base, long e) {
-  const uint8_t* p = static_cast<const uint8_t*>(base) + e * (kF32 ? 4 : 2);
-  cp_async16(dst, p);
-  if constexpr (kF32) cp_async16(dst + 16, p + 16);
+__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src) {
+  cp_async16(dst, src);
+  if constexpr (kF32) cp_async16(dst + 16, src + 16);
 }
+
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) { st_shared_v4(addr, make_uint4(0u, 0u, 0u, 0u)); }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
