@@ -266,14 +266,11 @@ __global__ void __launch_bounds__(256, 3) moe_combine_backward_kernel(const uint
           if constexpr (kQuant) {
             const float s = __shfl_sync(0xffffffffu, own_s, k, 16), y = __shfl_sync(0xffffffffu, own_y, k, 16);
             uint32_t c[2];
-            if (tiny) {
-              float o[8];
+            Pair8 o;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = wk * g[e];
-              fp8g::quant::encode_group(o, s, c);
-            } else {
-              fp8g::quant::normal_codes_of_product(gp, wk, s, y, c);
-            }
+            for (int e = 0; e < 4; ++e) o.v[e] = mul2(gp.v[e], both(wk));
+            if (tiny) fp8g::quant::any_codes(o, s, c);
+            else fp8g::quant::normal_codes(o, s, y, c);
             if (in) fp8g::quant::store_code_words(q + static_cast<long>(p) * N + 8L * j, c);
           } else if (in) {
             float o[8];

@@ -38,23 +38,19 @@ using namespace fp8g::rows;
 using fp8g::cluster_ctarank;
 using fp8g::cluster_sync_all;
 using fp8g::quant::quantize8;
+using fp8g::st_shared_v4;
 
 constexpr int kMaxH = 16384;
 
-// A row belongs to a cluster of 1, 2 or 4 CTAs, each with a run of its columns
-// and a thread per 8 of them.  The rows stream through shared memory in kStages
-// stages: a thread copies its own columns of a later row (cp.async) as soon as
-// it has read its columns of the current one, so kStages - 1 rows are under
-// way per CTA while one is worked on, without barriers or waits on other
-// threads.  The parameters' values of a thread's columns stay in registers for
-// all of the CTA's rows.
-constexpr int kBackwardStages = 3;
-__host__ __device__ constexpr int forward_stages(bool f32) { return f32 ? 3 : 4; }
-
+// A row belongs to a cluster of 1, 2 or 4 CTAs, each with a run of its columns;
+// a thread has V vectors of 8 columns, blockDim vectors apart.  The rows stream
+// through shared memory in D stages: a thread copies its own columns of a later
+// row (cp.async) before it works on the current one, so D - 1 rows are under way
+// per CTA, without barriers or waits on other threads.
 struct Shape {
   int rows, H;
-  int cols;      // columns of a CTA (the last of a cluster may have fewer)
-  uint32_t pitch;  // bytes of one row's part in shared memory (whole warps of it)
+  int cols;        // columns of a CTA (the last of a cluster may have fewer)
+  uint32_t pitch;  // bytes of one row's part in shared memory (whole vectors of all threads)
 };
 
 struct Params {
@@ -90,118 +86,142 @@ __device__ __forceinline__ float rms_factor(float sum, float inv_h, float eps) {
 }
 
 // The stages of a CTA: kTensors rows each, walked in step with its rows.  A
-// thread's slots of a tensor that is not there, and all slots of a thread
-// without columns, are zeroed once and never copied to, so the arithmetic needs
-// no conditions.  Addresses advance by additions only: with a multiplication
-// per row and tensor, a third of the instructions were address arithmetic.
-template <bool kF32, int kTensors, int kStages>
+// thread's slots of a tensor that is not there, and of vectors behind the row's
+// end, are zeroed once and never copied to, so the arithmetic needs no
+// conditions.  Addresses advance by additions only: with a multiplication per
+// row and tensor, a third of the instructions were address arithmetic.
+template <bool kF32, int V, int kTensors, int D>
 struct Stream {
-  const uint8_t* src[kTensors];  // this thread's columns of the next row to fetch
-  uint32_t slot, stage_bytes, pitch;
-  uint32_t put, get_at;  // stages to fill and to read, as offsets
-  long step_bytes;       // bytes from a CTA's row to its next
-  long next;             // the next row to fetch
-  bool in, third, fourth;
+  uint32_t slot, pitch, put, get;  // this thread's first slot; stages to fill and to read, as offsets
+  long fetch_at;                   // bytes from a tensor's start to this thread's columns of the next row to fetch
+  long step_bytes;                 // from a CTA's row to its next
+  long left;                       // rows that are still to be fetched
+  bool in[V];
 
   static constexpr int kVec = kF32 ? 32 : 16;  // bytes of 8 elements
+  // bytes between a thread's vectors
+  __device__ __forceinline__ uint32_t apart() const { return blockDim.x * kVec; }
 
   __device__ __forceinline__ void init(const void* const (&t)[kTensors], const uint8_t* smem, const Shape& S, int col0,
-                                       bool has_columns, long row0, long step) {
+                                       long row0, long step) {
     slot = fp8g::smem_u32(smem) + threadIdx.x * kVec;
     pitch = S.pitch;
-    stage_bytes = kTensors * pitch;
-    put = get_at = 0;
-    in = has_columns;
-    next = row0;
-    const long row_bytes = static_cast<long>(S.H) * (kVec / 8);
-    step_bytes = step * row_bytes;
+    put = get = 0;
+    fetch_at = (row0 * S.H + col0) * (kVec / 8) + threadIdx.x * kVec;
+    step_bytes = step * S.H * (kVec / 8);
+    left = (S.rows - row0 + step - 1) / step;
 #pragma unroll
-    for (int i = 0; i < kTensors; ++i) {
-      if (!in || !t[i]) {
+    for (int v = 0; v < V; ++v) {
+      const int col = 8 * (threadIdx.x + v * blockDim.x);
+      in[v] = col < S.cols && col0 + col < S.H;
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-          st_shared_zero16(slot + s * stage_bytes + i * pitch);
-          if constexpr (kF32) st_shared_zero16(slot + s * stage_bytes + i * pitch + 16);
+      for (int i = 0; i < kTensors; ++i) {
+        if (in[v] && t[i]) continue;
+#pragma unroll
+        for (int s = 0; s < D; ++s) {
+          const uint32_t at = slot + (s * kTensors + i) * pitch + v * apart();
+          st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
+          if constexpr (kF32) st_shared_v4(at + 16, make_uint4(0u, 0u, 0u, 0u));
         }
       }
-      src[i] = static_cast<const uint8_t*>(t[i]) + (row0 * row_bytes + static_cast<long>(col0) * (kVec / 8) + threadIdx.x * kVec);
     }
-    third = kTensors > 2 && t[kTensors > 2 ? 2 : 0];
-    fourth = kTensors > 3 && t[kTensors > 3 ? 3 : 0];
-    if (kTensors == 2) third = t[1] != nullptr;  // the forward pass's residual
   }
 
-  // Copies this thread's part of the next row, if there is one, into the next stage.
-  __device__ __forceinline__ void fetch(int rows, long step) {
-    if (next < rows && in) {
-      const uint32_t at = slot + put;
-      copy8<kF32>(at, src[0]);
-      if constexpr (kTensors == 2) {
-        if (third) copy8<kF32>(at + pitch, src[1]);
-      } else {
-        copy8<kF32>(at + pitch, src[1]);
-        if (third) copy8<kF32>(at + 2 * pitch, src[2]);
-        if (fourth) copy8<kF32>(at + 3 * pitch, src[3]);
+  // Copies this thread's part of the next row, if there is one, into the next
+  // stage.  The first `always` tensors are there.
+  __device__ __forceinline__ void fetch(const void* const (&t)[kTensors], int always) {
+    if (left > 0) {
+#pragma unroll
+      for (int i = 0; i < kTensors; ++i) {
+        if (i >= always && !t[i]) continue;
+        const uint8_t* p = static_cast<const uint8_t*>(t[i]) + fetch_at;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (in[v]) copy8<kF32>(slot + put + i * pitch + v * apart(), p + v * apart());
       }
     }
     cp_commit();
-    next += step;
-#pragma unroll
-    for (int i = 0; i < kTensors; ++i) src[i] += step_bytes;
-    put = put == (kStages - 1) * stage_bytes ? 0 : put + stage_bytes;
+    --left;
+    fetch_at += step_bytes;
+    put = put == (D - 1) * kTensors * pitch ? 0 : put + kTensors * pitch;
   }
 
-  __device__ __forceinline__ Pair8 get(int tensor) const {
-    return pairs_of<kF32>(load8_shared<kF32>(slot + get_at + tensor * pitch));
+  __device__ __forceinline__ Pair8 load(int tensor, int v) const {
+    return pairs_of<kF32>(load8_shared<kF32>(slot + get + tensor * pitch + v * apart()));
   }
 
-  __device__ __forceinline__ void advance() { get_at = get_at == (kStages - 1) * stage_bytes ? 0 : get_at + stage_bytes; }
+  __device__ __forceinline__ void advance() { get = get == (D - 1) * kTensors * pitch ? 0 : get + kTensors * pitch; }
 };
 
 // Stores a thread's 8 values of a row, rounded once.
 template <bool kF32>
-__device__ __forceinline__ void put8(uint8_t* at, const Pair8& p) {
+__device__ __forceinline__ void put8(void* base, long at, const Pair8& p) {
   float f[8];
   values_of(p, f);
-  store8<kF32>(at, 0, f);
+  store8<kF32>(static_cast<uint8_t*>(base) + at, 0, f);
 }
 
-template <bool kF32, int kC, bool kQuant>
-__global__ void __launch_bounds__(1024) norm_residual_kernel(const void* y, const void* h, Shape S, Params P, void* h_out,
-                                                             void* z, uint8_t* q, float* sa, int ld_sa) {
+// 8 FP32 parameters of a thread's columns in its own slot of shared memory.
+__device__ __forceinline__ void keep8(uint32_t at, const Pair8& p) {
+  float f[8];
+  values_of(p, f);
+  st_shared_v4(at, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+  st_shared_v4(at + 16, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+}
+
+__device__ __forceinline__ Pair8 kept8(uint32_t at) { return pairs_of<true>(load8_shared<true>(at)); }
+
+// Stages: two where two CTAs share an SM (bf16, two vectors a thread), else three.
+__host__ __device__ constexpr int forward_stages(bool f32, int vecs) { return !f32 && vecs == 2 ? 2 : 3; }
+constexpr int kBackwardStages = 3;
+
+// Threads and CTAs per SM that the registers are limited for.
+constexpr int max_threads(int vecs) { return vecs == 2 ? 512 : 256; }
+
+template <bool kF32, int V, int kC, bool kQuant>
+__global__ void __launch_bounds__(max_threads(V), V == 2 ? 2 : 4)
+    norm_residual_kernel(const void* y, const void* h, Shape S, Params P, void* h_out, void* z, uint8_t* q, float* sa,
+                         int ld_sa) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ RowSum<1, kC> sm;
-  constexpr int D = forward_stages(kF32);
+  constexpr int D = forward_stages(kF32, V);
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
-  const int col0 = rank * S.cols, col = col0 + 8 * threadIdx.x;
-  const bool in = 8 * static_cast<int>(threadIdx.x) < S.cols && col < S.H;
-  Stream<kF32, 2, D> src;
-  src.init({y, h}, dyn, S, col0, in, row0, step);
+  const int col0 = rank * S.cols;
+  const void* const tensors[2] = {y, h};
+  Stream<kF32, V, 2, D> src;
+  src.init(tensors, dyn, S, col0, row0, step);
+  long at = src.fetch_at;  // this thread's columns of the current row
 #pragma unroll
-  for (int s = 0; s < D - 1; ++s) src.fetch(S.rows, step);
-  const long first = (row0 * S.H + col) * (src.kVec / 8);
-  uint8_t *h_at = static_cast<uint8_t*>(h_out) + first, *z_at = static_cast<uint8_t*>(z) + first;
-  uint8_t* q_at = q + (row0 * S.H + col);
-  float* sa_at = sa + (static_cast<long>(col / 128) * ld_sa + row0);
-  Pair8 pw, a;
-  column_params(P, col, in, pw, a);
+  for (int s = 0; s < D - 1; ++s) src.fetch(tensors, 1);
+  // post_w (g per channel) stays in shared memory, pre_w in registers
+  const uint32_t a_at = fp8g::smem_u32(dyn) + 2 * D * S.pitch + threadIdx.x * 32;
+  Pair8 pw[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    Pair8 a;
+    column_params(P, col0 + 8 * (threadIdx.x + v * blockDim.x), src.in[v], pw[v], a);
+    keep8(a_at + v * blockDim.x * 32, a);
+  }
   if constexpr (kC > 1) cluster_sync_all();
   const float inv_h = 1.f / static_cast<float>(S.H);
   int turn = 0;
   for (long row = row0; row < S.rows; row += step) {
-    src.fetch(S.rows, step);
+    src.fetch(tensors, 1);
     cp_wait<D - 1>();
-    const Pair8 yv = src.get(0);
-    Pair8 hv = src.get(1);
+    Pair8 yv[V], hv[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) yv[v] = src.load(0, v), hv[v] = src.load(1, v);
     src.advance();
     float f = P.scale;
     if (P.gate_kind == FP8G_GATE_TOKEN) f *= __ldg(P.gate + row);
     float ss[1];
     if (P.post_w) {
-      uint64_t acc = mul2(yv.v[0], yv.v[0]);
+      uint64_t acc = 0;
 #pragma unroll
-      for (int i = 1; i < 4; ++i) acc = fma2(yv.v[i], yv.v[i], acc);
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = fma2(yv[v].v[i], yv[v].v[i], acc);
       ss[0] = sum2(acc);
       row_sum<1, kC>(ss, sm, turn, rank);
       f *= rms_factor(ss[0], inv_h, P.eps);
@@ -209,38 +229,44 @@ __global__ void __launch_bounds__(1024) norm_residual_kernel(const void* y, cons
     uint64_t acc = 0;
     const uint64_t ff = both(f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hv.v[i] = fma2(a.v[i], mul2(yv.v[i], ff), hv.v[i]);
-      acc = fma2(hv.v[i], hv.v[i], acc);
+    for (int v = 0; v < V; ++v) {
+      const Pair8 a = kept8(a_at + v * blockDim.x * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hv[v].v[i] = fma2(a.v[i], mul2(yv[v].v[i], ff), hv[v].v[i]);
+        acc = fma2(hv[v].v[i], hv[v].v[i], acc);
+      }
+      if (src.in[v]) put8<kF32>(h_out, at + v * src.apart(), hv[v]);
     }
-    if (in) put8<kF32>(h_at, hv);
-    h_at += src.step_bytes;
     ss[0] = sum2(acc);
     row_sum<1, kC>(ss, sm, turn, rank);
     const uint64_t r1 = both(rms_factor(ss[0], inv_h, P.eps));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) hv.v[i] = mul2(pw.v[i], mul2(hv.v[i], r1));
-    if constexpr (kQuant) {
-      // 16 lanes hold a 1x128 group (a CTA's columns are whole groups: a half-warp is all in or all out)
-      float v[8], amax = 0.f;
-      values_of(hv, v);
+    for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+      for (int i = 0; i < 4; ++i) hv[v].v[i] = mul2(pw[v].v[i], mul2(hv[v].v[i], r1));
+      if constexpr (kQuant) {
+        // 16 lanes hold a 1x128 group (a CTA's columns are whole groups: a half-warp is all in or all out)
+        float x[8], amax = 0.f;
+        values_of(hv[v], x);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      float sc;
-      uint32_t c[2];
-      quantize8(v, amax, sc, c);
-      if (in) {
-        fp8g::quant::store_code_words(q_at, c);
-        if ((threadIdx.x & 15) == 0) *sa_at = sc;
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        float sc;
+        uint32_t c[2];
+        quantize8(hv[v], amax, sc, c);
+        if (src.in[v]) {
+          // a code's offset in q is its element's: at counts bytes of the input type
+          fp8g::quant::store_code_words(q + (at + v * src.apart()) / (src.kVec / 8), c);
+          if ((threadIdx.x & 15) == 0)
+            sa[static_cast<long>((col0 + 8 * (threadIdx.x + v * blockDim.x)) / 128) * ld_sa + row] = sc;
+        }
+      } else {
+        if (src.in[v]) put8<kF32>(z, at + v * src.apart(), hv[v]);
       }
-      q_at += step * S.H;
-      sa_at += step;
-    } else {
-      if (in) put8<kF32>(z_at, hv);
-      z_at += src.step_bytes;
     }
+    at += src.step_bytes;
   }
 }
 
@@ -248,86 +274,83 @@ __global__ void __launch_bounds__(1024) norm_residual_kernel(const void* y, cons
 // over rows that all parameter gradients come from: dz n and dh u (with the
 // gate per token: g dh u).  They leave as one partial row per cluster,
 // part[2][clusters][H], which norm_param_grad_kernel adds in a fixed order (no
-// atomics: the same bits every run).
-// kThreads: 896 (72 registers a thread, enough for its sums, parameters and
-// values) or 1024.
-template <bool kF32, int kC, int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_residual_backward_kernel(const void* dz, const void* dh_out, const void* h,
-                                                                      const void* y, Shape S, Params P, void* dh, void* dy,
-                                                                      float* __restrict__ dgate, float* __restrict__ part) {
+// atomics: the same bits every run).  Those sums belong to columns, so a thread
+// has to keep its columns for all rows, and a row takes the whole CTA.
+template <bool kF32, int V, int kC>
+__global__ void __launch_bounds__(max_threads(V), V == 2 ? 1 : 3)
+    norm_residual_backward_kernel(const void* dz, const void* dh_out, const void* h, const void* y, Shape S, Params P,
+                                  void* dh, void* dy, float* __restrict__ dgate, float* __restrict__ part) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ RowSum<4, kC> sm4;
   __shared__ RowSum<1, kC> sm1;
   constexpr int D = kBackwardStages;
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
-  const int col0 = rank * S.cols, col = col0 + 8 * threadIdx.x;
-  const bool in = 8 * static_cast<int>(threadIdx.x) < S.cols && col < S.H;
-  Stream<kF32, 4, D> src;
-  src.init({h, y, dz, dh_out}, dyn, S, col0, in, row0, step);
+  const int col0 = rank * S.cols;
+  const void* const tensors[4] = {h, y, dz, dh_out};
+  Stream<kF32, V, 4, D> src;
+  src.init(tensors, dyn, S, col0, row0, step);
+  long at = src.fetch_at;
 #pragma unroll
-  for (int s = 0; s < D - 1; ++s) src.fetch(S.rows, step);
-  const long first = (row0 * S.H + col) * (src.kVec / 8);
-  uint8_t *dh_at = static_cast<uint8_t*>(dh) + first, *dy_at = static_cast<uint8_t*>(dy) + first;
-  Pair8 pw;
-  // s post_w (g per channel), used once a row: kept in shared memory, which
-  // leaves the registers to what every phase needs
-  const uint32_t a_at = src.slot - threadIdx.x * src.kVec + D * src.stage_bytes + threadIdx.x * 32;
-  {
+  for (int s = 0; s < D - 1; ++s) src.fetch(tensors, 2);
+  // s post_w (g per channel) stays in shared memory, pre_w and the sums in registers
+  const uint32_t a_at = fp8g::smem_u32(dyn) + 4 * D * S.pitch + threadIdx.x * 32;
+  Pair8 pw[V], acc_pre[V] = {}, acc_u[V] = {};
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
     Pair8 a;
-    column_params(P, col, in, pw, a);
+    column_params(P, col0 + 8 * (threadIdx.x + v * blockDim.x), src.in[v], pw[v], a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) a.v[i] = mul2(a.v[i], both(P.scale));
-    float v[8];
-    values_of(a, v);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      fp8g::st_shared_v4(a_at + 16 * i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+    keep8(a_at + v * blockDim.x * 32, a);
   }
   if constexpr (kC > 1) cluster_sync_all();
   const float inv_h = 1.f / static_cast<float>(S.H);
   const bool token = P.gate_kind == FP8G_GATE_TOKEN;
-  Pair8 acc_pre = {}, acc_u = {};
   int turn4 = 0, turn1 = 0;
   for (long row = row0; row < S.rows; row += step) {
-    src.fetch(S.rows, step);
+    src.fetch(tensors, 2);
     cp_wait<D - 1>();
-    const Pair8 hv = src.get(0);
-    Pair8 yv = src.get(1), g = src.get(2);  // g: dz, then dh, then du
-    uint64_t hh = 0, dn = 0, yy = 0;              // h'^2, (dz pre_w) h', y^2
+    Pair8 hv[V], yv[V], g[V];         // g: dz, then dh, then du
+    uint64_t hh = 0, dn = 0, yy = 0;  // h'^2, (dz pre_w) h', y^2
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hh = fma2(hv.v[i], hv.v[i], hh);
-      dn = fma2(mul2(g.v[i], pw.v[i]), hv.v[i], dn);
-      yy = fma2(yv.v[i], yv.v[i], yy);
+    for (int v = 0; v < V; ++v) {
+      hv[v] = src.load(0, v), yv[v] = src.load(1, v), g[v] = src.load(2, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hh = fma2(hv[v].v[i], hv[v].v[i], hh);
+        dn = fma2(mul2(g[v].v[i], pw[v].v[i]), hv[v].v[i], dn);
+        yy = fma2(yv[v].v[i], yv[v].v[i], yy);
+      }
     }
     float st[4] = {sum2(hh), sum2(dn), sum2(yy), 0.f};
     row_sum<4, kC>(st, sm4, turn4, rank);
     const float r1 = rms_factor(st[0], inv_h, P.eps);
     const float r2 = P.post_w ? rms_factor(st[2], inv_h, P.eps) : 1.f;
     const float gt = token ? __ldg(P.gate + row) : 1.f;
-    const Pair8 t = src.get(3);
-    src.advance();
     const uint64_t rr1 = both(r1), rr2 = both(r2);
     const uint64_t rm = both(-r1 * (st[1] * r1 * inv_h));  // - r1 <dz pre_w n>
+    uint64_t du_u = 0;                                     // a dh u
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t n = mul2(hv.v[i], rr1);
-      acc_pre.v[i] = fma2(g.v[i], n, acc_pre.v[i]);
-      g.v[i] = fma2(n, rm, fma2(mul2(g.v[i], pw.v[i]), rr1, t.v[i]));
-    }
-    if (in) put8<kF32>(dh_at, g);
-    dh_at += src.step_bytes;
-    const Pair8 a = pairs_of<true>(load8_shared<true>(a_at));
-    uint64_t du_u = 0;  // a dh u
+    for (int v = 0; v < V; ++v) {
+      const Pair8 t = src.load(3, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      yv.v[i] = mul2(yv.v[i], rr2);
-      acc_u.v[i] = fma2(token ? mul2(g.v[i], both(gt)) : g.v[i], yv.v[i], acc_u.v[i]);
-      g.v[i] = mul2(g.v[i], a.v[i]);
-      du_u = fma2(g.v[i], yv.v[i], du_u);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t n = mul2(hv[v].v[i], rr1);
+        acc_pre[v].v[i] = fma2(g[v].v[i], n, acc_pre[v].v[i]);
+        g[v].v[i] = fma2(n, rm, fma2(mul2(g[v].v[i], pw[v].v[i]), rr1, t.v[i]));
+      }
+      if (src.in[v]) put8<kF32>(dh, at + v * src.apart(), g[v]);
+      const Pair8 a = kept8(a_at + v * blockDim.x * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        yv[v].v[i] = mul2(yv[v].v[i], rr2);
+        acc_u[v].v[i] = fma2(token ? mul2(g[v].v[i], both(gt)) : g[v].v[i], yv[v].v[i], acc_u[v].v[i]);
+        g[v].v[i] = mul2(g[v].v[i], a.v[i]);
+        du_u = fma2(g[v].v[i], yv[v].v[i], du_u);
+      }
     }
+    src.advance();
     float m2 = 0.f;  // <du u>
     if (P.post_w || token) {
       float dot[1] = {sum2(du_u)};
@@ -337,20 +360,27 @@ __global__ void __launch_bounds__(kThreads) norm_residual_backward_kernel(const 
     }
     const uint64_t f = both(r2 * gt), um = both(-r2 * m2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) g.v[i] = fma2(g.v[i], f, mul2(yv.v[i], um));
-    if (in) put8<kF32>(dy_at, g);
-    dy_at += src.step_bytes;
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[v].v[i] = fma2(g[v].v[i], f, mul2(yv[v].v[i], um));
+      if (src.in[v]) put8<kF32>(dy, at + v * src.apart(), g[v]);
+    }
+    at += src.step_bytes;
   }
-  if (part && in) {
-    float* p = part + row0 * S.H + col;
-    float* pu = p + step * S.H;
-    float v[8];
-    values_of(acc_pre, v);
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    values_of(acc_u, v);
-    reinterpret_cast<float4*>(pu)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(pu)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  if (part) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!src.in[v]) continue;
+      float* p = part + row0 * S.H + col0 + 8 * (threadIdx.x + v * blockDim.x);
+      float* pu = p + step * S.H;
+      float x[8];
+      values_of(acc_pre[v], x);
+      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+      values_of(acc_u[v], x);
+      reinterpret_cast<float4*>(pu)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(pu)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
   }
 }
 
@@ -399,6 +429,7 @@ constexpr int kOneLaunch = 256;    // up to so many partial rows one launch sums
 // How a row of H columns is split and how many clusters walk the rows.
 struct Plan {
   Shape S;
+  int vecs;      // vectors of 8 columns per thread
   int ctas;      // per cluster
   int threads;
   int smem;
@@ -407,20 +438,23 @@ struct Plan {
 
 constexpr int kSms = 148;
 constexpr int kSmemPerSm = 225 << 10;
+// rows up to so many columns get one vector a thread: more, shorter CTAs
+constexpr int kNarrow = 2048;
 
 // tensors: rows streamed per stage.  The cluster grows until a CTA has at most
-// 1024 threads and its stages fit the shared memory; narrow rows get as many
-// CTAs per SM as 72 registers a thread and their stages allow.
-Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int more_per_thread) {
+// max_threads and its stages fit the shared memory; as many CTAs per SM as the
+// registers of `sm_threads` threads and the stages allow.
+Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int vecs, int sm_threads) {
   Plan p{};
+  p.vecs = vecs;
   for (p.ctas = 1;; p.ctas *= 2) {
-    const int units = (H / unit + p.ctas - 1) / p.ctas;
-    p.threads = (units * unit / 8 + 31) / 32 * 32;
-    p.S = Shape{rows, H, units * unit, static_cast<uint32_t>(p.threads * 8 * esz)};
-    p.smem = tensors * stages * static_cast<int>(p.S.pitch) + more_per_thread * p.threads;
-    if (p.ctas == 4 || (p.threads <= 1024 && p.smem <= kSmemPerSm)) break;
+    const int cols = ((H + unit - 1) / unit + p.ctas - 1) / p.ctas * unit;
+    p.threads = (cols / 8 + 32 * vecs - 1) / (32 * vecs) * 32;
+    p.S = Shape{rows, H, cols, static_cast<uint32_t>(p.threads * vecs * 8 * esz)};
+    p.smem = tensors * stages * static_cast<int>(p.S.pitch) + 32 * vecs * p.threads;
+    if (p.ctas == 4 || (p.threads <= max_threads(vecs) && p.smem <= kSmemPerSm)) break;
   }
-  const int per_sm = std::max(1, std::min({32, 896 / p.threads, kSmemPerSm / (p.smem + 1024)}));
+  const int per_sm = std::max(1, std::min({32, sm_threads / p.threads, kSmemPerSm / (p.smem + 2048)}));
   p.clusters = std::max(1L, std::min<long>(rows, static_cast<long>(kSms) * per_sm / p.ctas));
   return p;
 }
@@ -429,11 +463,14 @@ Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int mo
 // same order whether it leaves as values or as codes, in either type (1 CTA up
 // to H = 8192, 2 above).
 Plan forward_plan(int rows, int H, int dtype) {
-  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 2, forward_stages(dtype == FP8G_IN_F32), H % 128 == 0 ? 128 : 8, 0);
+  const bool f32 = dtype == FP8G_IN_F32;
+  const int vecs = H <= kNarrow ? 1 : 2;
+  return plan_of(rows, H, f32 ? 4 : 2, 2, forward_stages(f32, vecs), H % 128 == 0 ? 128 : 8, vecs, 1024);
 }
 
 Plan backward_plan(int rows, int H, int dtype) {
-  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 4, kBackwardStages, 8, 32);
+  const int vecs = H <= kNarrow ? 1 : 2;
+  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 4, kBackwardStages, 8, vecs, vecs == 1 ? 768 : 512);
 }
 
 // Launches the kernel for the plan's cluster size.
@@ -493,13 +530,18 @@ extern "C" int fp8g_norm_residual(const void* y, const void* h, int dtype, int r
   const Plan p = forward_plan(rows, H, dtype);
   const Params P{post_w, gate, pre_w, gate_kind, scale, eps};
   auto go = [&](auto kernel) { return launch(p, kernel, stream, y, h, p.S, P, h_out, z, q, sa, ld_sa); };
+  auto by_split = [&](auto narrow, auto one, auto two) { return p.vecs == 1 ? go(narrow) : p.ctas == 1 ? go(one) : go(two); };
   cudaError_t e;
   if (dtype == FP8G_IN_F32)
-    e = q ? (p.ctas == 1 ? go(norm_residual_kernel<true, 1, true>) : go(norm_residual_kernel<true, 2, true>))
-          : (p.ctas == 1 ? go(norm_residual_kernel<true, 1, false>) : go(norm_residual_kernel<true, 2, false>));
+    e = q ? by_split(norm_residual_kernel<true, 1, 1, true>, norm_residual_kernel<true, 2, 1, true>,
+                     norm_residual_kernel<true, 2, 2, true>)
+          : by_split(norm_residual_kernel<true, 1, 1, false>, norm_residual_kernel<true, 2, 1, false>,
+                     norm_residual_kernel<true, 2, 2, false>);
   else
-    e = q ? (p.ctas == 1 ? go(norm_residual_kernel<false, 1, true>) : go(norm_residual_kernel<false, 2, true>))
-          : (p.ctas == 1 ? go(norm_residual_kernel<false, 1, false>) : go(norm_residual_kernel<false, 2, false>));
+    e = q ? by_split(norm_residual_kernel<false, 1, 1, true>, norm_residual_kernel<false, 2, 1, true>,
+                     norm_residual_kernel<false, 2, 2, true>)
+          : by_split(norm_residual_kernel<false, 1, 1, false>, norm_residual_kernel<false, 2, 1, false>,
+                     norm_residual_kernel<false, 2, 2, false>);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return FP8G_ERR_CUDA;
@@ -539,15 +581,15 @@ extern "C" int fp8g_norm_residual_backward(const void* dz, const void* dh_out, c
   if (rows > 0) {
     auto go = [&](auto kernel) { return launch(p, kernel, stream, dz, dh_out, h_out, y, p.S, P, dh, dy, dgate, part); };
     cudaError_t e;
-    const bool wide = p.threads > 896;
-    if (dtype == FP8G_IN_F32)  // a cluster of 2 or 4 has at most 512 threads a CTA
-      e = p.ctas == 1   ? go(norm_residual_backward_kernel<true, 1, 896>)
-          : p.ctas == 2 ? go(norm_residual_backward_kernel<true, 2, 896>)
-                        : go(norm_residual_backward_kernel<true, 4, 896>);
-    else if (p.ctas == 1)
-      e = wide ? go(norm_residual_backward_kernel<false, 1, 1024>) : go(norm_residual_backward_kernel<false, 1, 896>);
+    if (dtype == FP8G_IN_F32)
+      e = p.vecs == 1   ? go(norm_residual_backward_kernel<true, 1, 1>)
+          : p.ctas == 1 ? go(norm_residual_backward_kernel<true, 2, 1>)
+          : p.ctas == 2 ? go(norm_residual_backward_kernel<true, 2, 2>)
+                        : go(norm_residual_backward_kernel<true, 2, 4>);
     else
-      e = wide ? go(norm_residual_backward_kernel<false, 2, 1024>) : go(norm_residual_backward_kernel<false, 2, 896>);
+      e = p.vecs == 1   ? go(norm_residual_backward_kernel<false, 1, 1>)
+          : p.ctas == 1 ? go(norm_residual_backward_kernel<false, 2, 1>)
+                        : go(norm_residual_backward_kernel<false, 2, 2>);
     if (e != cudaSuccess) {
       (void)cudaGetLastError();
       return FP8G_ERR_CUDA;

@@ -23,41 +23,39 @@ constexpr float kInv448 = 1.0f / kE4M3Max;    // rounded to nearest
 // The scale of a group whose amax is 0 or at least kTinyAmax.
 __device__ __forceinline__ float normal_scale(float amax) { return amax > 0.f ? quotient_rn(amax, kE4M3Max, kInv448) : 1.f; }
 
-// Codes of 8 values, packed 4 per word, with scale s and y = fl(1 / s).
-__device__ __forceinline__ void normal_codes(const float (&v)[8], float s, float y, uint32_t (&c)[2]) {
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quotient_rn(v[i], s, y);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) c[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | (e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16);
-}
-
-// The same for 8 products w * x, two at a time in packed FP32x2 instructions
-// (each half rounds like its scalar form).
-__device__ __forceinline__ void normal_codes_of_product(const rows::Pair8& x, float w, float s, float y, uint32_t (&c)[2]) {
+// Codes of 8 values, packed 4 per word, with scale s and y = fl(1 / s): the
+// quotients of quotient_rn, two at a time in packed FP32x2 instructions (each
+// half rounds like its scalar form).
+__device__ __forceinline__ void normal_codes(const rows::Pair8& x, float s, float y, uint32_t (&c)[2]) {
   using namespace rows;
-  const uint64_t ww = both(w), yy = both(y), ns = both(-s);
+  const uint64_t yy = both(y), ns = both(-s);
   float q[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t v = mul2(x.v[i], ww);
-    uint64_t r = mul2(v, yy);
-    r = fma2(fma2(r, ns, v), yy, r);
-    r = fma2(fma2(r, ns, v), yy, r);
+    uint64_t r = mul2(x.v[i], yy);
+    r = fma2(fma2(r, ns, x.v[i]), yy, r);
+    r = fma2(fma2(r, ns, x.v[i]), yy, r);
     float a, b, va, vb;
-    split2(r, a, b), split2(v, va, vb);
+    split2(r, a, b), split2(x.v[i], va, vb);
     q[2 * i] = copysignf(a, va), q[2 * i + 1] = copysignf(b, vb);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) c[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | (e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16);
 }
 
+// The general path, for groups of any magnitude.
+__device__ __forceinline__ void any_codes(const rows::Pair8& x, float s, uint32_t (&c)[2]) {
+  float v[8];
+  rows::values_of(x, v);
+  encode_group(v, s, c);
+}
+
 // Scale and codes of a lane's 8 values of a group with largest magnitude amax.
 // All 32 lanes call it.
-__device__ __forceinline__ void quantize8(const float (&v)[8], float amax, float& s, uint32_t (&c)[2]) {
+__device__ __forceinline__ void quantize8(const rows::Pair8& v, float amax, float& s, uint32_t (&c)[2]) {
   if (__any_sync(0xffffffffu, amax > 0.f && amax < kTinyAmax)) {
     s = scale_of(amax);
-    encode_group(v, s, c);
+    any_codes(v, s, c);
   } else {
     s = normal_scale(amax);
     normal_codes(v, s, __frcp_rn(s), c);
