@@ -419,7 +419,7 @@ extern "C" int fp8g_moe_combine_backward(const uint16_t* dout, const uint16_t* D
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel, int group) {
     const int smem = 2 * (group + 1) * threads * 16;  // at most 72 KB
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 72 << 10);
+    e = allow_smem(kernel);
     if (e == cudaSuccess)
       kernel<<<grid, threads, smem, stream>>>(dout, D, N, pos, w, T, topk, dD, q, sa, ld_sa, dw, blocks * 128, blocks, pads,
                                               err);

@@ -385,22 +385,25 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 1 : 3)
 }
 
 // Sums of partial rows part[2][P][H] over P.  A CTA takes 32 columns and the
-// partial rows of its blockIdx.y: its 8 warps every eighth row each, 8 loads
-// at a time, then the warps' sums in warp order.  Many partial rows (narrow
+// partial rows of its blockIdx.y: its 32 warps every 32nd row each, 8 loads
+// at a time, then the warps' sums in warp order (8192 x 7168, 148 partial rows:
+// latency of one or two rounds of loads).  Many partial rows (narrow
 // rows have many CTAs) are summed in two launches: to out[2][gridDim.y][H]
 // first, then to the gradients (kLast).
+constexpr int kSumWarps = 32;
+
 template <bool kLast>
-__global__ void __launch_bounds__(256) norm_param_grad_kernel(const float* __restrict__ part, int P, int H, int per,
+__global__ void __launch_bounds__(32 * kSumWarps) norm_param_grad_kernel(const float* __restrict__ part, int P, int H, int per,
                                                               float* __restrict__ out, Params prm, float* dpre,
                                                               float* dpost, float* dgate) {
-  __shared__ float s[2][8][32];
+  __shared__ float s[2][kSumWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   const int p0 = blockIdx.y * per, p1 = min(P, p0 + per);
   float a = 0.f, b = 0.f;
   if (col < H) {
 #pragma unroll 8
-    for (int p = p0 + w; p < p1; p += 8) {
+    for (int p = p0 + w; p < p1; p += kSumWarps) {
       a += part[static_cast<long>(p) * H + col];
       b += part[(static_cast<long>(P) + p) * H + col];
     }
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(256) norm_param_grad_kernel(const float* __res
   if (w != 0 || col >= H) return;
   a = b = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a += s[0][i][lane], b += s[1][i][lane];
+  for (int i = 0; i < kSumWarps; ++i) a += s[0][i][lane], b += s[1][i][lane];
   if constexpr (kLast) {
     const bool channel = prm.gate_kind == FP8G_GATE_CHANNEL;
     if (dpre) dpre[col] = a;
@@ -423,8 +426,8 @@ __global__ void __launch_bounds__(256) norm_param_grad_kernel(const float* __res
   }
 }
 
-constexpr int kPartsPerSum = 64;   // partial rows of a CTA in the first of two launches
-constexpr int kOneLaunch = 256;    // up to so many partial rows one launch sums them all
+constexpr int kPartsPerSum = 256;  // partial rows of a CTA in the first of two launches
+constexpr int kOneLaunch = 1024;   // up to so many partial rows one launch sums them all
 
 // How a row of H columns is split and how many clusters walk the rows.
 struct Plan {
@@ -437,7 +440,7 @@ struct Plan {
 };
 
 constexpr int kSms = 148;
-constexpr int kSmemPerSm = 225 << 10;
+constexpr int kSmemPerSm = 224 << 10;  // of 227 KB: the static part takes up to 5 KB where the stages leave more
 // rows up to so many columns get one vector a thread: more, shorter CTAs
 constexpr int kNarrow = 2048;
 
@@ -454,8 +457,12 @@ Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int ve
     p.smem = tensors * stages * static_cast<int>(p.S.pitch) + 32 * vecs * p.threads;
     if (p.ctas == 4 || (p.threads <= max_threads(vecs) && p.smem <= kSmemPerSm)) break;
   }
-  const int per_sm = std::max(1, std::min({32, sm_threads / p.threads, kSmemPerSm / (p.smem + 2048)}));
-  p.clusters = std::max(1L, std::min<long>(rows, static_cast<long>(kSms) * per_sm / p.ctas));
+  const int per_sm = std::max(1, std::min({32, sm_threads / p.threads, kSmemPerSm / p.smem}));
+  // no more clusters than rows, and no more than it takes for all to have the
+  // same number of rows or one less
+  const long most = std::max(1L, static_cast<long>(kSms) * per_sm / p.ctas);
+  const long rounds = std::max(1L, (rows + most - 1) / most);
+  p.clusters = std::max(1L, (rows + rounds - 1) / rounds);
   return p;
 }
 
@@ -476,11 +483,8 @@ Plan backward_plan(int rows, int H, int dtype) {
 // Launches the kernel for the plan's cluster size.
 template <typename... KArgs, typename... Args>
 cudaError_t launch(const Plan& p, void (*kernel)(KArgs...), cudaStream_t stream, Args... args) {
-  if (p.smem > 47 << 10) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = fp8g::rows::allow_smem(kernel);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(static_cast<unsigned>(p.clusters * p.ctas), 1, 1);
@@ -601,12 +605,12 @@ extern "C" int fp8g_norm_residual_backward(const void* dz, const void* dh_out, c
     if (n > kOneLaunch) {
       const int sums = (n + kPartsPerSum - 1) / kPartsPerSum;
       float* out = part + 2L * n * H;
-      norm_param_grad_kernel<false><<<dim3(groups, sums), 256, 0, stream>>>(part, n, H, kPartsPerSum, out, P, nullptr, nullptr,
+      norm_param_grad_kernel<false><<<dim3(groups, sums), 32 * kSumWarps, 0, stream>>>(part, n, H, kPartsPerSum, out, P, nullptr, nullptr,
                                                                             nullptr);
       part = out;
       n = sums;
     }
-    norm_param_grad_kernel<true><<<groups, 256, 0, stream>>>(part, n, H, n, nullptr, P, dpre_w, dpost_w, dgate);
+    norm_param_grad_kernel<true><<<groups, 32 * kSumWarps, 0, stream>>>(part, n, H, n, nullptr, P, dpre_w, dpost_w, dgate);
   }
   if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
   return FP8G_OK;

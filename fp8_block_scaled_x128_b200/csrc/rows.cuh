@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "ptx.cuh"
 
@@ -243,6 +244,38 @@ __device__ __forceinline__ Raw8<kF32> load8_shared(uint32_t addr) {
 
 // ---------------------------------------------------------------- host
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Lets a kernel use all of an SM's shared memory that its static part leaves,
+// once per kernel and device (the calls would cost every launch a microsecond).
+template <typename... KArgs>
+inline cudaError_t allow_smem(void (*kernel)(KArgs...)) {
+  struct Seen {
+    const void* fn;
+    uint64_t devices;
+  };
+  static std::mutex mu;
+  static Seen seen[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  Seen* at = nullptr;
+  for (Seen& s : seen) {
+    if (s.fn == reinterpret_cast<const void*>(kernel) || !s.fn) {
+      at = &s;
+      break;
+    }
+  }
+  if (at && at->fn && dev < 64 && (at->devices >> dev & 1)) return cudaSuccess;
+  int most = 0;
+  cudaFuncAttributes fa;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  if ((e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kernel))) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           most - static_cast<int>(fa.sharedSizeBytes));
+  if (e == cudaSuccess && at && dev < 64) at->fn = reinterpret_cast<const void*>(kernel), at->devices |= 1ull << dev;
+  return e;
+}
 
 // Streaming multiprocessors of the current device, -1 if there is none.
 inline int sm_count() {

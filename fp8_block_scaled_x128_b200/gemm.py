@@ -7,7 +7,6 @@ the shared library is missing, importing this module raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 
@@ -347,44 +346,63 @@ def moe_combine(D, pos, w, T, topk, out=None, stream=None):
 
 
 def _shaped(t, dt, shape, name):
-    """t, if it is a contiguous CUDA tensor of this type and shape."""
-    if not t.is_cuda or t.dtype != dt or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    """t, if it is a contiguous CUDA tensor of this type and shape (a tuple)."""
+    if t.dtype != dt or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous CUDA tensor of {dt} {tuple(shape)}, got {t.dtype} "
                         f"{tuple(t.shape)} on {t.device}")
     return t
 
 
 def _rows(t, name):
-    if not t.is_cuda or t.dtype not in _IN_DTYPE or not t.is_contiguous() or t.dim() != 2:
+    if t.dtype not in _IN_DTYPE or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous 2-D CUDA tensor of bfloat16 or float32, got {t.dtype} "
                         f"{tuple(t.shape)} on {t.device}")
     return t
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
+def _all_on(dev, names, *tensors):
+    """Refuses tensors on another device than dev (None stands for a missing one).
+    These calls are made once per layer and decoded token: the checks are kept
+    short, a dict of every operand cost 2 us a call."""
+    for i, t in enumerate(tensors):
+        if t is not None and t.device != dev:
+            raise ValueError(f"all operands must be on one device: {names.split()[i]} is on {t.device}, expected {dev}")
+
+
+# the raw handle of a device's current stream; without the Stream object of
+# torch.cuda.current_stream where torch has the short way
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _On:
     """Runs a call under its operands' device and, if a stream is given, under
     that stream, so that what the call allocates belongs to the stream it runs
-    on.  Gives the raw stream."""
-    if stream is None:
-        if dev.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream(dev).cuda_stream
-        else:
-            with torch.cuda.device(dev):
-                yield torch.cuda.current_stream(dev).cuda_stream
-        return
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the operands on {dev}")
-    with torch.cuda.stream(stream):
-        yield stream.cuda_stream
+    on.  Entering gives the raw stream."""
+    __slots__ = ("dev", "stream", "ctx")
+
+    def __init__(self, dev, stream):
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the operands on {dev}")
+        self.dev, self.stream, self.ctx = dev, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.dev)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return _current_raw(self.dev.index) if self.stream is None else self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _tensors(**tensors):
-    return {name: t for name, t in tensors.items() if t is not None}
 
 
 def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
@@ -399,8 +417,9 @@ def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
     topk, G, Mmax = int(topk), int(G), int(Mmax)
     R = T * topk
     _shaped(expert, torch.int32, (R,), "expert")
-    dev = _one_device(x=x, expert=expert)
-    with _on(dev, stream) as raw:
+    dev = x.device
+    _all_on(dev, "expert", expert)
+    with _On(dev, stream) as raw:
         if out is None:
             ld = (Mmax + 3) // 4 * 4
             out = (torch.empty((G, Mmax, K), dtype=torch.uint8, device=dev),
@@ -410,7 +429,7 @@ def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
         _shaped(A, torch.uint8, (G, Mmax, K), "A")
         _shaped(sa, torch.float32, (G, K // 128, sa.shape[-1]), "sa")
         _shaped(pos, torch.int32, (R,), "pos"), _shaped(masked_m, torch.int32, (G,), "masked_m")
-        _one_device(x=x, A=A, sa=sa, pos=pos, masked_m=masked_m)
+        _all_on(dev, "A sa pos masked_m", A, sa, pos, masked_m)
         _check(lib.fp8g_moe_dispatch_masked(x.data_ptr(), _IN_DTYPE[x.dtype], T, K, expert.data_ptr(), topk, G, Mmax,
                                             A.data_ptr(), sa.data_ptr(), sa.shape[-1], pos.data_ptr(),
                                             masked_m.data_ptr(), raw), "fp8g_moe_dispatch_masked")
@@ -429,15 +448,16 @@ def moe_permute(x, expert, topk, G, blocks=None, out=None, stream=None):
     R = T * topk
     _shaped(expert, torch.int32, (R,), "expert")
     nb = moe_blocks(T, topk, G) if blocks is None else int(blocks)
-    dev = _one_device(x=x, expert=expert)
-    with _on(dev, stream) as raw:
+    dev = x.device
+    _all_on(dev, "expert", expert)
+    with _On(dev, stream) as raw:
         if out is None:
             out = (torch.empty((nb * 128, N), dtype=x.dtype, device=dev),
                    torch.empty(R, dtype=torch.int32, device=dev), torch.empty(nb, dtype=torch.int32, device=dev))
         xs, pos, mi = out
         _shaped(xs, x.dtype, (nb * 128, N), "xs")
         _shaped(pos, torch.int32, (R,), "pos"), _shaped(mi, torch.int32, (nb,), "m_indices")
-        _one_device(x=x, xs=xs, pos=pos, m_indices=mi)
+        _all_on(dev, "xs pos m_indices", xs, pos, mi)
         _check(lib.fp8g_moe_permute(x.data_ptr(), _IN_DTYPE[x.dtype], T, N, expert.data_ptr(), topk, G, nb,
                                     xs.data_ptr(), pos.data_ptr(), mi.data_ptr(), raw), "fp8g_moe_permute")
     return xs, pos, mi
@@ -452,11 +472,12 @@ def moe_permute_backward(dxs, pos, T, topk, out=None, stream=None):
     T, topk = int(T), int(topk)
     _layout_rows(M, "dxs")
     _shaped(pos, torch.int32, (T * topk,), "pos")
-    dev = _one_device(dxs=dxs, pos=pos)
-    with _on(dev, stream) as raw:
+    dev = dxs.device
+    _all_on(dev, "pos", pos)
+    with _On(dev, stream) as raw:
         dx = torch.empty((T, N), dtype=dxs.dtype, device=dev) if out is None else out
         _shaped(dx, dxs.dtype, (T, N), "out")
-        _one_device(dxs=dxs, out=dx)
+        _all_on(dev, "out", dx)
         _check(lib.fp8g_moe_permute_backward(dxs.data_ptr(), _IN_DTYPE[dxs.dtype], M // 128, N, pos.data_ptr(), T,
                                              topk, dx.data_ptr(), raw), "fp8g_moe_permute_backward")
     return dx
@@ -482,8 +503,9 @@ def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, str
     _shaped(dout, torch.bfloat16, (T, N), "dout"), _shaped(pos, torch.int32, (T * topk,), "pos")
     if w is not None:
         _shaped(w, torch.float32, (T * topk,), "w")
-    dev = _one_device(**_tensors(dout=dout, D=D, pos=pos, w=w))
-    with _on(dev, stream) as raw:
+    dev = dout.device
+    _all_on(dev, "D pos w", D, pos, w)
+    with _On(dev, stream) as raw:
         if out is None:
             dw = None if w is None else torch.empty(T * topk, dtype=torch.float32, device=dev)
             if quantize:
@@ -502,7 +524,7 @@ def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, str
             raise ValueError("dw: an output exactly if w is given")
         if dw is not None:
             _shaped(dw, torch.float32, (T * topk,), "dw")
-        _one_device(**_tensors(dout=dout, dD=dD, q=q, sa=sa, dw=dw))
+        _all_on(dev, "dD q sa dw", dD, q, sa, dw)
         _check(lib.fp8g_moe_combine_backward(dout.data_ptr(), D.data_ptr(), N, pos.data_ptr(), _addr(w), T, topk,
                                              M // 128, _addr(dD), _addr(q), _addr(sa),
                                              0 if sa is None else sa.shape[-1], _addr(dw), raw),
@@ -513,9 +535,10 @@ def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, str
 def _norm_params(y, post_weight, gate, pre_weight):
     """Checks the parameters of rows y; the kind of the gate."""
     rows, H = y.shape
-    for name, p in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if p is not None:
-            _shaped(p, torch.float32, (H,), name)
+    if post_weight is not None:
+        _shaped(post_weight, torch.float32, (H,), "post_weight")
+    if pre_weight is not None:
+        _shaped(pre_weight, torch.float32, (H,), "pre_weight")
     if gate is None:
         return 0
     if gate.dim() == 1:
@@ -540,8 +563,9 @@ def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=
     if h is not None:
         _shaped(h, y.dtype, (rows, H), "h")
     kind = _norm_params(y, post_weight, gate, pre_weight)
-    dev = _one_device(**_tensors(y=y, h=h, post_weight=post_weight, gate=gate, pre_weight=pre_weight))
-    with _on(dev, stream) as raw:
+    dev = y.device
+    _all_on(dev, "h post_weight gate pre_weight", h, post_weight, gate, pre_weight)
+    with _On(dev, stream) as raw:
         if out is None:
             if quantize:
                 out = (torch.empty_like(y), torch.empty((rows, H), dtype=torch.uint8, device=dev),
@@ -556,7 +580,7 @@ def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=
             h_out, z = out
             _shaped(z, y.dtype, (rows, H), "z")
         _shaped(h_out, y.dtype, (rows, H), "h_out")
-        _one_device(**_tensors(y=y, h_out=h_out, z=z, q=q, sa=sa))
+        _all_on(dev, "h_out z q sa", h_out, z, q, sa)
         _check(lib.fp8g_norm_residual(y.data_ptr(), _addr(h), _IN_DTYPE[y.dtype], rows, H, _addr(post_weight),
                                       _addr(gate), kind, scale, _addr(pre_weight), eps, h_out.data_ptr(), _addr(z),
                                       _addr(q), _addr(sa), 0 if sa is None else sa.shape[-1], raw),
@@ -579,9 +603,9 @@ def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, sc
         if t is not None:
             _shaped(t, y.dtype, (rows, H), name)
     kind = _norm_params(y, post_weight, gate, pre_weight)
-    dev = _one_device(**_tensors(y=y, h_out=h_out, dz=dz, dh_out=dh_out, post_weight=post_weight, gate=gate,
-                                 pre_weight=pre_weight))
-    with _on(dev, stream) as raw:
+    dev = y.device
+    _all_on(dev, "h_out dz dh_out post_weight gate pre_weight", h_out, dz, dh_out, post_weight, gate, pre_weight)
+    with _On(dev, stream) as raw:
         if out is None:
             out = (torch.empty_like(y), torch.empty_like(y), *(None if p is None else torch.empty_like(p)
                                                                 for p in (pre_weight, post_weight, gate)))
@@ -598,8 +622,7 @@ def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, sc
             workspace = torch.empty(need // 4, dtype=torch.float32, device=dev)
         elif workspace is not None:
             _dev(workspace, torch.float32, "workspace")
-        _one_device(**_tensors(y=y, dh=dh, dy=dy, dpre_weight=dpre, dpost_weight=dpost, dgate=dgate,
-                               workspace=workspace))
+        _all_on(dev, "dh dy dpre_weight dpost_weight dgate workspace", dh, dy, dpre, dpost, dgate, workspace)
         _check(lib.fp8g_norm_residual_backward(_addr(dz), _addr(dh_out), h_out.data_ptr(), y.data_ptr(),
                                                _IN_DTYPE[y.dtype], rows, H, _addr(post_weight), _addr(gate), kind,
                                                scale, _addr(pre_weight), eps, dh.data_ptr(), dy.data_ptr(), _addr(dpre),
