@@ -158,32 +158,32 @@ __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* _
 
 // ---------------------------------------------------------------- combine backward
 // A CTA takes a token and walks its row in steps of blockDim vectors (8 columns
-// a thread); the slots of a step come in groups of kGroup.  A thread copies its
-// own vectors of the next (step, group) -- dout and each slot's D row -- into
-// shared memory (cp.async) before it works on the current one, so the loads of
-// kGroup + 1 rows are under way all the time without holding registers.
+// a thread), four slots at a time.  A thread copies its own vectors of the next
+// four slots' D rows (and of dout) into shared memory (cp.async) before it works
+// on the current ones, so loads are under way all the time without holding
+// registers.  FP32x2 instructions: with bf16 out the kernel is bound by HBM, with
+// codes out by instructions issued.
 //
 // kQuant: the rows leave as e4m3 codes and 1x128 scales; 16 lanes hold a group
 // of columns.  Its largest |w x| is |w| times its largest |x|, rounded once
 // (rounding is monotonic), so one reduction over x serves every slot; lane k of
 // the 16 forms slot k's scale and its reciprocal, and the others get them by
 // shuffle: the divisions are done once per group and slot, not in every lane.
-template <bool kQuant, int kGroup, int kGroups>
-__global__ void __launch_bounds__(256, 3) moe_combine_backward_kernel(const uint16_t* __restrict__ dout,
-                                                                      const uint16_t* __restrict__ D, int N,
-                                                                      const int32_t* __restrict__ pos,
-                                                                      const float* __restrict__ w, int T, int topk,
-                                                                      uint16_t* __restrict__ dD, uint8_t* __restrict__ q,
-                                                                      float* __restrict__ sa, int ld_sa,
-                                                                      float* __restrict__ dw, int M, int blocks, int pads,
-                                                                      uint32_t* err) {
+constexpr int kGroup = 4;
+
+template <bool kQuant, int kGroups>
+__global__ void __launch_bounds__(256, kGroups == 4 ? 2 : 4)
+    moe_combine_backward_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ D, int N,
+                                const int32_t* __restrict__ pos, const float* __restrict__ w, int T, int topk,
+                                uint16_t* __restrict__ dD, uint8_t* __restrict__ q, float* __restrict__ sa, int ld_sa,
+                                float* __restrict__ dw, int M, int blocks, int pads, uint32_t* err) {
   constexpr int kSlots = kGroup * kGroups;
   extern __shared__ __align__(16) uint8_t dyn[];  // two stages of kGroup + 1 vectors a thread
-  __shared__ uint32_t bits[kPadBlocks * 4];
+  __shared__ __align__(16) int s_pos[kSlots];
+  __shared__ __align__(16) float s_w[kSlots];
   __shared__ float s_dot[8][kSlots];
-  __shared__ int s_pos[kSlots];
-  __shared__ float s_w[kSlots];
   if (static_cast<int>(blockIdx.x) < pads) {
+    __shared__ uint32_t bits[kPadBlocks * 4];
     int b0, b1, slice;
     pad_range(blockIdx.x, pads, blocks, b0, b1, slice);
     pad_blocks(pos, static_cast<long>(T) * topk, b0, b1, slice, bits, err, [&](long row) {
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256, 3) moe_combine_backward_kernel(const uint
     return;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int own = lane & 15;  // the slot of a group whose scale this lane forms
+  const int own = min(lane & 15, kSlots - 1);  // the slot whose scale this lane forms
   const int per_row = N / 8, step = blockDim.x;
   const int items = (per_row + step - 1) / step * kGroups;
   const uint32_t pitch = step * 16, stage = (kGroup + 1) * pitch;
@@ -208,82 +208,85 @@ __global__ void __launch_bounds__(256, 3) moe_combine_backward_kernel(const uint
       s_w[k] = k < topk && w ? __ldg(w + t * topk + k) : 1.f;
     }
     __syncthreads();
-    auto fetch = [&](int i) {
+    const uint16_t* dout_t = dout + t * N;
+    auto fetch = [&](int i) {  // i % kGroups is a constant where it is called
       const int j = i / kGroups * step + threadIdx.x;
       if (i < items && j < per_row) {
         const uint32_t at = slot0 + (i & 1) * stage;
-        cp_async16(at, dout + t * N + 8L * j);
+        if (i % kGroups == 0) cp_async16(at, dout_t + 8L * j);
         if (dw) {
+          const int4 p4 = *reinterpret_cast<const int4*>(s_pos + i % kGroups * kGroup);
+          const int p[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
-          for (int k = 0; k < kGroup; ++k) {
-            const int p = s_pos[i % kGroups * kGroup + k];
-            if (p >= 0) cp_async16(at + (k + 1) * pitch, D + static_cast<long>(p) * N + 8L * j);
-          }
+          for (int k = 0; k < kGroup; ++k)
+            if (p[k] >= 0) cp_async16(at + (k + 1) * pitch, D + static_cast<long>(p[k]) * N + 8L * j);
         }
       }
       cp_commit();
     };
-    float dot[kSlots];
+    uint64_t dot[kSlots];
 #pragma unroll
-    for (int k = 0; k < kSlots; ++k) dot[k] = 0.f;
+    for (int k = 0; k < kSlots; ++k) dot[k] = 0;
     fetch(0);
     for (int i0 = 0; i0 < items; i0 += kGroups) {
+      const int j = i0 / kGroups * step + threadIdx.x;
+      const bool in = j < per_row;
+      Pair8 g;
+      float own_s = 1.f, own_y = 1.f;
+      bool tiny = false;
 #pragma unroll
       for (int gi = 0; gi < kGroups; ++gi) {
         const int i = i0 + gi;
         fetch(i + 1);
         cp_wait<1>();
-        const int j = i0 / kGroups * step + threadIdx.x;
-        const bool in = j < per_row;
         const uint32_t at = slot0 + (i & 1) * stage;
-        float g[8];
-        unpack8<false>(in ? load8_shared<false>(at) : zero8<false>(), g);
-        Pair8 gp;
+        if (gi == 0) {
+          g = pairs_of<false>(in ? load8_shared<false>(at) : zero8<false>());
+          // every thread of a warp takes part in the groups' maxima and scales
+          if constexpr (kQuant) {
+            float x[8], amax = 0.f;
+            values_of(g, x);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) gp.v[c] = pack2(g[2 * c], g[2 * c + 1]);
-        // every thread of a warp takes part in the groups' maxima and scales
-        float own_s = 1.f, own_y = 1.f;
-        bool tiny = false;
-        if constexpr (kQuant) {
-          float amax = 0.f;
+            for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(x[c]));
 #pragma unroll
-          for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(g[c]));
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const int own_slot = gi * kGroup + (own < kGroup ? own : 0);
-          const int own_p = s_pos[own_slot];
-          amax *= fabsf(s_w[own_slot]);
-          tiny = __any_sync(0xffffffffu, amax > 0.f && amax < fp8g::quant::kTinyAmax);
-          own_s = tiny ? fp8g::quant::scale_of(amax) : fp8g::quant::normal_scale(amax);
-          own_y = __frcp_rn(own_s);
-          if (in && own < kGroup && own_p >= 0) sa[static_cast<long>(j >> 4) * ld_sa + own_p] = own_s;
+            for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            amax *= fabsf(s_w[own]);
+            tiny = __any_sync(0xffffffffu, amax > 0.f && amax < fp8g::quant::kTinyAmax);
+            own_s = tiny ? fp8g::quant::scale_of(amax) : fp8g::quant::normal_scale(amax);
+            own_y = __frcp_rn(own_s);
+            const int p = s_pos[own];
+            if (in && (lane & 15) < kSlots && p >= 0) sa[static_cast<long>(j >> 4) * ld_sa + p] = own_s;
+          }
         }
+        const int4 p4 = *reinterpret_cast<const int4*>(s_pos + gi * kGroup);
+        const float4 w4 = *reinterpret_cast<const float4*>(s_w + gi * kGroup);
+        const int p[4] = {p4.x, p4.y, p4.z, p4.w};
+        const float wk[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) {
-          const int p = s_pos[gi * kGroup + k];
-          if (p < 0) continue;  // the same for the whole CTA
-          const float wk = s_w[gi * kGroup + k];
+          if (p[k] < 0) continue;  // the same for the whole CTA
+          const long e = static_cast<long>(p[k]) * N + 8L * j;
+          Pair8 o;
           if constexpr (kQuant) {
-            const float s = __shfl_sync(0xffffffffu, own_s, k, 16), y = __shfl_sync(0xffffffffu, own_y, k, 16);
+            const float s = __shfl_sync(0xffffffffu, own_s, gi * kGroup + k, 16);
+            const float y = __shfl_sync(0xffffffffu, own_y, gi * kGroup + k, 16);
             uint32_t c[2];
-            Pair8 o;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o.v[e] = mul2(gp.v[e], both(wk));
+            for (int m = 0; m < 4; ++m) o.v[m] = mul2(g.v[m], both(-wk[k]));  // the quantiser takes negatives
             if (tiny) fp8g::quant::any_codes(o, s, c);
             else fp8g::quant::normal_codes(o, s, y, c);
-            if (in) fp8g::quant::store_code_words(q + static_cast<long>(p) * N + 8L * j, c);
-          } else if (in) {
-            float o[8];
+            if (in) fp8g::quant::store_code_words(q + e, c);
+          } else {
+            float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = wk * g[e];
-            store8<false>(dD, static_cast<long>(p) * N + 8L * j, o);
+            for (int m = 0; m < 4; ++m) o.v[m] = mul2(g.v[m], both(wk[k]));
+            values_of(o, f);
+            if (in) store8<false>(dD, e, f);
           }
           if (dw && in) {
             const Pair8 d = pairs_of<false>(load8_shared<false>(at + (k + 1) * pitch));
-            uint64_t acc = mul2(gp.v[0], d.v[0]);
 #pragma unroll
-            for (int c = 1; c < 4; ++c) acc = fma2(gp.v[c], d.v[c], acc);
-            dot[gi * kGroup + k] += sum2(acc);
+            for (int m = 0; m < 4; ++m) dot[gi * kGroup + k] = fma2(g.v[m], d.v[m], dot[gi * kGroup + k]);
           }
         }
       }
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(256, 3) moe_combine_backward_kernel(const uint
 #pragma unroll
       for (int k = 0; k < kSlots; ++k) {
         if (k >= topk) continue;
-        const float sum = warp_sum(dot[k]);
+        const float sum = warp_sum(sum2(dot[k]));
         if (lane == 0) s_dot[warp][k] = sum;
       }
     }
@@ -417,19 +420,18 @@ extern "C" int fp8g_moe_combine_backward(const uint16_t* dout, const uint16_t* D
   const unsigned grid = static_cast<unsigned>(pads + std::min<long>(T, 32L * sms));
   const int threads = row_threads(N / 8);
   cudaError_t e = cudaSuccess;
-  auto go = [&](auto kernel, int group) {
-    const int smem = 2 * (group + 1) * threads * 16;  // at most 72 KB
+  auto go = [&](auto kernel) {
     e = allow_smem(kernel);
     if (e == cudaSuccess)
-      kernel<<<grid, threads, smem, stream>>>(dout, D, N, pos, w, T, topk, dD, q, sa, ld_sa, dw, blocks * 128, blocks, pads,
-                                              err);
+      kernel<<<grid, threads, 2 * (kGroup + 1) * threads * 16, stream>>>(dout, D, N, pos, w, T, topk, dD, q, sa, ld_sa, dw,
+                                                                        blocks * 128, blocks, pads, err);
   };
   if (q)
-    by_topk(topk, [&] { go(moe_combine_backward_kernel<true, 4, 1>, 4); },
-            [&] { go(moe_combine_backward_kernel<true, 8, 1>, 8); }, [&] { go(moe_combine_backward_kernel<true, 8, 2>, 8); });
+    by_topk(topk, [&] { go(moe_combine_backward_kernel<true, 1>); }, [&] { go(moe_combine_backward_kernel<true, 2>); },
+            [&] { go(moe_combine_backward_kernel<true, 4>); });
   else
-    by_topk(topk, [&] { go(moe_combine_backward_kernel<false, 4, 1>, 4); },
-            [&] { go(moe_combine_backward_kernel<false, 8, 1>, 8); }, [&] { go(moe_combine_backward_kernel<false, 8, 2>, 8); });
+    by_topk(topk, [&] { go(moe_combine_backward_kernel<false, 1>); }, [&] { go(moe_combine_backward_kernel<false, 2>); },
+            [&] { go(moe_combine_backward_kernel<false, 4>); });
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return FP8G_ERR_CUDA;

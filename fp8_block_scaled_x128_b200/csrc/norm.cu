@@ -240,7 +240,9 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 2 : 4)
     }
     ss[0] = sum2(acc);
     row_sum<1, kC>(ss, sm, turn, rank);
-    const uint64_t r1 = both(rms_factor(ss[0], inv_h, P.eps));
+    // the quantiser takes the negatives of its values
+    const float r = rms_factor(ss[0], inv_h, P.eps);
+    const uint64_t r1 = both(kQuant ? -r : r);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll

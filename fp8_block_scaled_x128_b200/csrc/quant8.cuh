@@ -23,42 +23,45 @@ constexpr float kInv448 = 1.0f / kE4M3Max;    // rounded to nearest
 // The scale of a group whose amax is 0 or at least kTinyAmax.
 __device__ __forceinline__ float normal_scale(float amax) { return amax > 0.f ? quotient_rn(amax, kE4M3Max, kInv448) : 1.f; }
 
-// Codes of 8 values, packed 4 per word, with scale s and y = fl(1 / s): the
-// quotients of quotient_rn, two at a time in packed FP32x2 instructions (each
-// half rounds like its scalar form).
-__device__ __forceinline__ void normal_codes(const rows::Pair8& x, float s, float y, uint32_t (&c)[2]) {
+// Codes of 8 values, packed 4 per word, with scale s and y = fl(1 / s), given
+// the values' negatives.  The quotients are quotient_rn's, two at a time in
+// packed FP32x2 instructions (each half rounds like its scalar form), with the
+// residual taken as q s - x: then a zero quotient keeps its sign through both
+// corrections (q s - x = +0 for either zero, and q - (+0) y = q), so no value's
+// sign has to be restored.
+__device__ __forceinline__ void normal_codes(const rows::Pair8& neg, float s, float y, uint32_t (&c)[2]) {
   using namespace rows;
-  const uint64_t yy = both(y), ns = both(-s);
+  const uint64_t ss = both(s), ny = both(-y);
   float q[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint64_t r = mul2(x.v[i], yy);
-    r = fma2(fma2(r, ns, x.v[i]), yy, r);
-    r = fma2(fma2(r, ns, x.v[i]), yy, r);
-    float a, b, va, vb;
-    split2(r, a, b), split2(x.v[i], va, vb);
-    q[2 * i] = copysignf(a, va), q[2 * i + 1] = copysignf(b, vb);
+    uint64_t r = mul2(neg.v[i], ny);
+    r = fma2(fma2(r, ss, neg.v[i]), ny, r);
+    r = fma2(fma2(r, ss, neg.v[i]), ny, r);
+    split2(r, q[2 * i], q[2 * i + 1]);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) c[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | (e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16);
 }
 
 // The general path, for groups of any magnitude.
-__device__ __forceinline__ void any_codes(const rows::Pair8& x, float s, uint32_t (&c)[2]) {
+__device__ __forceinline__ void any_codes(const rows::Pair8& neg, float s, uint32_t (&c)[2]) {
   float v[8];
-  rows::values_of(x, v);
+  rows::values_of(neg, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = -v[i];
   encode_group(v, s, c);
 }
 
-// Scale and codes of a lane's 8 values of a group with largest magnitude amax.
-// All 32 lanes call it.
-__device__ __forceinline__ void quantize8(const rows::Pair8& v, float amax, float& s, uint32_t (&c)[2]) {
+// Scale and codes of a lane's 8 values of a group with largest magnitude amax,
+// given the values' negatives.  All 32 lanes call it.
+__device__ __forceinline__ void quantize8(const rows::Pair8& neg, float amax, float& s, uint32_t (&c)[2]) {
   if (__any_sync(0xffffffffu, amax > 0.f && amax < kTinyAmax)) {
     s = scale_of(amax);
-    any_codes(v, s, c);
+    any_codes(neg, s, c);
   } else {
     s = normal_scale(amax);
-    normal_codes(v, s, __frcp_rn(s), c);
+    normal_codes(neg, s, __frcp_rn(s), c);
   }
 }
 
