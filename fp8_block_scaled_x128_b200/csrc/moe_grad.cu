@@ -172,15 +172,16 @@ __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* _
 constexpr int kGroup = 4;
 
 template <bool kQuant, int kGroups>
-__global__ void __launch_bounds__(256, kGroups == 4 ? 2 : 4)
+__global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1 ? 4 : 3)
     moe_combine_backward_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ D, int N,
                                 const int32_t* __restrict__ pos, const float* __restrict__ w, int T, int topk,
                                 uint16_t* __restrict__ dD, uint8_t* __restrict__ q, float* __restrict__ sa, int ld_sa,
                                 float* __restrict__ dw, int M, int blocks, int pads, uint32_t* err) {
   constexpr int kSlots = kGroup * kGroups;
   extern __shared__ __align__(16) uint8_t dyn[];  // two stages of kGroup + 1 vectors a thread
-  __shared__ __align__(16) int s_pos[kSlots];
-  __shared__ __align__(16) float s_w[kSlots];
+  __shared__ long s_row[kSlots];    // first element of each slot's row, -1 if it is dropped
+  __shared__ int s_pos[kSlots];
+  __shared__ float s_w[kSlots];
   __shared__ float s_dot[8][kSlots];
   if (static_cast<int>(blockIdx.x) < pads) {
     __shared__ uint32_t bits[kPadBlocks * 4];
@@ -198,50 +199,61 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : 4)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int own = min(lane & 15, kSlots - 1);  // the slot whose scale this lane forms
   const int per_row = N / 8, step = blockDim.x;
-  const int items = (per_row + step - 1) / step * kGroups;
+  const int steps = (per_row + step - 1) / step;
   const uint32_t pitch = step * 16, stage = (kGroup + 1) * pitch;
   const uint32_t slot0 = fp8g::smem_u32(dyn) + threadIdx.x * 16;
   for (long t = static_cast<long>(blockIdx.x) - pads; t < T; t += static_cast<long>(gridDim.x) - pads) {
     if (threadIdx.x < kSlots) {
       const int k = threadIdx.x;
-      s_pos[k] = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+      const int p = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+      s_pos[k] = p;
+      s_row[k] = p < 0 ? -1 : static_cast<long>(p) * N;
       s_w[k] = k < topk && w ? __ldg(w + t * topk + k) : 1.f;
     }
     __syncthreads();
-    const uint16_t* dout_t = dout + t * N;
-    auto fetch = [&](int i) {  // i % kGroups is a constant where it is called
-      const int j = i / kGroups * step + threadIdx.x;
-      if (i < items && j < per_row) {
-        const uint32_t at = slot0 + (i & 1) * stage;
-        if (i % kGroups == 0) cp_async16(at, dout_t + 8L * j);
-        if (dw) {
-          const int4 p4 = *reinterpret_cast<const int4*>(s_pos + i % kGroups * kGroup);
-          const int p[4] = {p4.x, p4.y, p4.z, p4.w};
-#pragma unroll
-          for (int k = 0; k < kGroup; ++k)
-            if (p[k] >= 0) cp_async16(at + (k + 1) * pitch, D + static_cast<long>(p[k]) * N + 8L * j);
+    // this thread's columns of the next vectors to fetch, and of the current ones
+    const uint16_t* dout_at = dout + t * N + 8 * threadIdx.x;
+    const uint16_t* D_at = D + 8 * threadIdx.x;
+    long col = 8 * threadIdx.x;
+    int fetch_j = threadIdx.x;
+    uint32_t put = slot0, get = slot0;
+    // copies the vectors of slots gi * kGroup ..; zeros for columns behind the
+    // row's end, whose products then add nothing
+    auto fetch = [&](int gi, bool there) {
+      if (there) {
+        const bool in = fetch_j < per_row;
+        if (gi == 0) {
+          if (in) cp_async16(put, dout_at);
+          else fp8g::st_shared_v4(put, make_uint4(0u, 0u, 0u, 0u));
         }
+        if (dw) {
+#pragma unroll
+          for (int k = 0; k < kGroup; ++k) {
+            const long row = s_row[gi * kGroup + k];
+            if (!in) fp8g::st_shared_v4(put + (k + 1) * pitch, make_uint4(0u, 0u, 0u, 0u));
+            else if (row >= 0) cp_async16(put + (k + 1) * pitch, D_at + row);
+          }
+        }
+        if (gi == kGroups - 1) dout_at += 8 * step, D_at += 8 * step, fetch_j += step;
       }
       cp_commit();
+      put = put == slot0 ? slot0 + stage : slot0;
     };
     uint64_t dot[kSlots];
 #pragma unroll
     for (int k = 0; k < kSlots; ++k) dot[k] = 0;
-    fetch(0);
-    for (int i0 = 0; i0 < items; i0 += kGroups) {
-      const int j = i0 / kGroups * step + threadIdx.x;
-      const bool in = j < per_row;
+    fetch(0, true);
+    for (int i = 0; i < steps; ++i, col += 8 * step) {
+      const bool in = col < N;
       Pair8 g;
       float own_s = 1.f, own_y = 1.f;
       bool tiny = false;
 #pragma unroll
       for (int gi = 0; gi < kGroups; ++gi) {
-        const int i = i0 + gi;
-        fetch(i + 1);
+        fetch((gi + 1) % kGroups, gi + 1 < kGroups || i + 1 < steps);
         cp_wait<1>();
-        const uint32_t at = slot0 + (i & 1) * stage;
         if (gi == 0) {
-          g = pairs_of<false>(in ? load8_shared<false>(at) : zero8<false>());
+          g = pairs_of<false>(load8_shared<false>(get));
           // every thread of a warp takes part in the groups' maxima and scales
           if constexpr (kQuant) {
             float x[8], amax = 0.f;
@@ -254,41 +266,52 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : 4)
             tiny = __any_sync(0xffffffffu, amax > 0.f && amax < fp8g::quant::kTinyAmax);
             own_s = tiny ? fp8g::quant::scale_of(amax) : fp8g::quant::normal_scale(amax);
             own_y = __frcp_rn(own_s);
-            const int p = s_pos[own];
-            if (in && (lane & 15) < kSlots && p >= 0) sa[static_cast<long>(j >> 4) * ld_sa + p] = own_s;
+            if (in && (lane & 15) < kSlots && s_pos[own] >= 0) sa[(col >> 7) * ld_sa + s_pos[own]] = own_s;
           }
         }
-        const int4 p4 = *reinterpret_cast<const int4*>(s_pos + gi * kGroup);
-        const float4 w4 = *reinterpret_cast<const float4*>(s_w + gi * kGroup);
-        const int p[4] = {p4.x, p4.y, p4.z, p4.w};
-        const float wk[4] = {w4.x, w4.y, w4.z, w4.w};
+        // Dropped slots are worked on like the others and only not stored: with
+        // no branch between the slots their instructions interleave.
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) {
-          if (p[k] < 0) continue;  // the same for the whole CTA
-          const long e = static_cast<long>(p[k]) * N + 8L * j;
-          Pair8 o;
-          if constexpr (kQuant) {
-            const float s = __shfl_sync(0xffffffffu, own_s, gi * kGroup + k, 16);
-            const float y = __shfl_sync(0xffffffffu, own_y, gi * kGroup + k, 16);
-            uint32_t c[2];
+          const Pair8 d = pairs_of<false>(load8_shared<false>(get + (k + 1) * pitch));
 #pragma unroll
-            for (int m = 0; m < 4; ++m) o.v[m] = mul2(g.v[m], both(-wk[k]));  // the quantiser takes negatives
-            if (tiny) fp8g::quant::any_codes(o, s, c);
-            else fp8g::quant::normal_codes(o, s, y, c);
-            if (in) fp8g::quant::store_code_words(q + e, c);
+          for (int m = 0; m < 4; ++m) dot[gi * kGroup + k] = fma2(g.v[m], d.v[m], dot[gi * kGroup + k]);
+        }
+        if constexpr (kQuant) {
+          uint32_t c[kGroup][2];
+          if (!tiny) {
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+              const float s = __shfl_sync(0xffffffffu, own_s, gi * kGroup + k, 16);
+              const float y = __shfl_sync(0xffffffffu, own_y, gi * kGroup + k, 16);
+              const uint64_t nw = both(-s_w[gi * kGroup + k]);  // the quantiser takes negatives
+              fp8g::quant::normal_codes(Pair8{mul2(g.v[0], nw), mul2(g.v[1], nw), mul2(g.v[2], nw), mul2(g.v[3], nw)}, s, y,
+                                        c[k]);
+            }
           } else {
-            float f[8];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) o.v[m] = mul2(g.v[m], both(wk[k]));
-            values_of(o, f);
-            if (in) store8<false>(dD, e, f);
+            for (int k = 0; k < kGroup; ++k) {
+              const float s = __shfl_sync(0xffffffffu, own_s, gi * kGroup + k, 16);
+              const uint64_t nw = both(-s_w[gi * kGroup + k]);
+              fp8g::quant::any_codes(Pair8{mul2(g.v[0], nw), mul2(g.v[1], nw), mul2(g.v[2], nw), mul2(g.v[3], nw)}, s, c[k]);
+            }
           }
-          if (dw && in) {
-            const Pair8 d = pairs_of<false>(load8_shared<false>(at + (k + 1) * pitch));
 #pragma unroll
-            for (int m = 0; m < 4; ++m) dot[gi * kGroup + k] = fma2(g.v[m], d.v[m], dot[gi * kGroup + k]);
+          for (int k = 0; k < kGroup; ++k) {
+            const long row = s_row[gi * kGroup + k];
+            if (in && row >= 0) fp8g::quant::store_code_words(q + row + col, c[k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kGroup; ++k) {
+            const long row = s_row[gi * kGroup + k];
+            const uint64_t ww = both(s_w[gi * kGroup + k]);
+            float f[8];
+            values_of(Pair8{mul2(g.v[0], ww), mul2(g.v[1], ww), mul2(g.v[2], ww), mul2(g.v[3], ww)}, f);
+            if (in && row >= 0) store8<false>(dD, row + col, f);
           }
         }
+        get = get == slot0 ? slot0 + stage : slot0;
       }
     }
     if (dw) {
@@ -299,11 +322,12 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : 4)
         if (lane == 0) s_dot[warp][k] = sum;
       }
     }
-    __syncthreads();  // also: everyone has read s_pos and s_w
+    const bool dropped = threadIdx.x < kSlots && s_pos[threadIdx.x] < 0;
+    __syncthreads();  // also: everyone has read the slots' rows and weights
     if (dw && static_cast<int>(threadIdx.x) < topk) {
       float sum = 0.f;
       for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) sum += s_dot[i][threadIdx.x];
-      dw[t * topk + threadIdx.x] = sum;
+      dw[t * topk + threadIdx.x] = dropped ? 0.f : sum;
     }
   }
 }
