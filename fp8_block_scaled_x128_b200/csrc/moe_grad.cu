@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restric
                                                           int blocks, int pads, uint32_t* err) {
   __shared__ uint32_t bits[kPadBlocks * 4];
   if (static_cast<int>(blockIdx.x) < pads) {
+    fp8g::grid_dependency_wait();  // pos
     int b0, b1, slice;
     pad_range(blockIdx.x, pads, blocks, b0, b1, slice);
     pad_blocks(pos, static_cast<long>(T) * topk, b0, b1, slice, bits, err, [&](long row) {
@@ -116,14 +117,26 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restric
     return;
   }
   const long items = static_cast<long>(T) * parts;
-  for (long i = static_cast<long>(blockIdx.x) - pads; i < items; i += static_cast<long>(gridDim.x) - pads) {
-    const long t = i / parts;
-    const int j = static_cast<int>(i - t * parts) * blockDim.x + threadIdx.x;
-    const uint4 v = j < vecs ? __ldcs(x + t * vecs + j) : make_uint4(0u, 0u, 0u, 0u);
+  long i = static_cast<long>(blockIdx.x) - pads;
+  auto vector_of = [&](long item) {  // this thread's vector of an item, -1 behind the row's end
+    const long t = item / parts;
+    const int j = static_cast<int>(item - t * parts) * blockDim.x + threadIdx.x;
+    return j < vecs ? t * vecs + j : -1L;
+  };
+  long at = i < items ? vector_of(i) : -1;
+  uint4 v = at >= 0 ? __ldcs(x + at) : make_uint4(0u, 0u, 0u, 0u);  // x does not come from the layout kernel
+  fp8g::grid_dependency_wait();                                     // pos does
+  while (i < items) {
+    const long t = i / parts, j = at - t * vecs;
 #pragma unroll
     for (int k = 0; k < kCap; ++k) {
       const int p = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
-      if (p >= 0 && j < vecs) __stcs(xs + static_cast<long>(p) * vecs + j, v);
+      if (p >= 0 && at >= 0) __stcs(xs + static_cast<long>(p) * vecs + j, v);
+    }
+    i += static_cast<long>(gridDim.x) - pads;
+    if (i < items) {
+      at = vector_of(i);
+      if (at >= 0) v = __ldcs(x + at);
     }
   }
 }
@@ -386,13 +399,18 @@ extern "C" int fp8g_moe_permute(const void* x, int x_dtype, int T, int N, const 
   const int pads = pad_ctas(blocks, sms);
   const int parts = static_cast<int>((vecs + 255) / 256);
   const unsigned grid = static_cast<unsigned>(pads + std::min<long>(static_cast<long>(T) * parts, 1 << 20));
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    kernel<<<grid, row_threads(vecs), 0, stream>>>(static_cast<const uint4*>(x), static_cast<int>(vecs), parts, T, topk, pos,
-                                                   static_cast<uint4*>(xs), blocks * 128, blocks, pads, err);
+    e = launch_behind(dim3(grid), row_threads(vecs), stream, kernel, static_cast<const uint4*>(x),
+                                 static_cast<int>(vecs), parts, T, topk, static_cast<const int32_t*>(pos),
+                                 static_cast<uint4*>(xs), blocks * 128, blocks, pads, err);
   };
   by_topk(topk, [&] { go(moe_permute_kernel<4>); }, [&] { go(moe_permute_kernel<8>); },
           [&] { go(moe_permute_kernel<kMaxTopk>); });
-  if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FP8G_ERR_CUDA;
+  }
   return FP8G_OK;
 }
 

@@ -173,18 +173,27 @@ __device__ __forceinline__ Pair8 kept8(uint32_t at) { return pairs_of<true>(load
 
 // Stages: two where two CTAs share an SM (bf16, two vectors a thread), else three.
 __host__ __device__ constexpr int forward_stages(bool f32, int vecs) { return !f32 && vecs == 2 ? 2 : 3; }
-constexpr int kBackwardStages = 3;
+// The backward pass: three for bf16 rows of one CTA, two where three do not fit.
+constexpr int kOneCta = 8192;  // columns of bf16 that one CTA takes
+constexpr int backward_stages(bool f32, int H) { return f32 || H > kOneCta ? 2 : 3; }
 
-// Threads and CTAs per SM that the registers are limited for.
-constexpr int max_threads(int vecs) { return vecs == 2 ? 512 : 256; }
+// Most threads of a CTA, and the registers a thread of the backward kernel may
+// use (the forward kernel: 64).  They leave nothing to be kept in local memory:
+// with the stages in shared memory the L1 cache has a few KB, and six words
+// spilled cost 8192 x 7168 180 us instead of 131.
+constexpr int kMaxThreads = 512;
+constexpr int backward_regs(bool f32, int vecs) { return vecs == 2 ? 128 : f32 ? 88 : 80; }
+// Threads of an SM whose registers fit: each of its four parts has 16384.
+constexpr int threads_at(int regs) { return 128 * (16384 / (32 * regs)); }
 
 template <bool kF32, int V, int kC, bool kQuant>
-__global__ void __launch_bounds__(max_threads(V), V == 2 ? 2 : 4)
+__global__ void __launch_bounds__(kMaxThreads, 2)
     norm_residual_kernel(const void* y, const void* h, Shape S, Params P, void* h_out, void* z, uint8_t* q, float* sa,
-                         int ld_sa) {
-  extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ RowSum<1, kC> sm;
+                         int ld_sa, uint32_t* err) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ RowSum<1, kC> sm_y, sm_h;
   constexpr int D = forward_stages(kF32, V);
+  row_sum_init(sm_y), row_sum_init(sm_h);
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
   const int col0 = rank * S.cols;
@@ -205,17 +214,17 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 2 : 4)
   }
   if constexpr (kC > 1) cluster_sync_all();
   const float inv_h = 1.f / static_cast<float>(S.H);
-  int turn = 0;
-  for (long row = row0; row < S.rows; row += step) {
+  bool gave_up = false;
+  unsigned it = 0;
+  for (long row = row0; row < S.rows; row += step, ++it) {
+    const float gt = P.gate_kind == FP8G_GATE_TOKEN ? __ldg(P.gate + row) : 1.f;  // used behind the first sum
     src.fetch(tensors, 1);
     cp_wait<D - 1>();
     Pair8 yv[V], hv[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) yv[v] = src.load(0, v), hv[v] = src.load(1, v);
     src.advance();
-    float f = P.scale;
-    if (P.gate_kind == FP8G_GATE_TOKEN) f *= __ldg(P.gate + row);
-    float ss[1];
+    float f = P.scale, ss[1];
     if (P.post_w) {
       uint64_t acc = 0;
 #pragma unroll
@@ -223,11 +232,11 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 2 : 4)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc = fma2(yv[v].v[i], yv[v].v[i], acc);
       ss[0] = sum2(acc);
-      row_sum<1, kC>(ss, sm, turn, rank);
+      row_sum(ss, sm_y, it, rank, gave_up, err);
       f *= rms_factor(ss[0], inv_h, P.eps);
     }
     uint64_t acc = 0;
-    const uint64_t ff = both(f);
+    const uint64_t ff = both(f * gt);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const Pair8 a = kept8(a_at + v * blockDim.x * 32);
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 2 : 4)
       if (src.in[v]) put8<kF32>(h_out, at + v * src.apart(), hv[v]);
     }
     ss[0] = sum2(acc);
-    row_sum<1, kC>(ss, sm, turn, rank);
+    row_sum(ss, sm_h, it, rank, gave_up, err);
     // the quantiser takes the negatives of its values
     const float r = rms_factor(ss[0], inv_h, P.eps);
     const uint64_t r1 = both(kQuant ? -r : r);
@@ -278,14 +287,22 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 2 : 4)
 // part[2][clusters][H], which norm_param_grad_kernel adds in a fixed order (no
 // atomics: the same bits every run).  Those sums belong to columns, so a thread
 // has to keep its columns for all rows, and a row takes the whole CTA.
-template <bool kF32, int V, int kC>
-__global__ void __launch_bounds__(max_threads(V), V == 2 ? 1 : 3)
+//
+// dy needs a sum over the row of a dh u, and dh the row's statistics.  One CTA
+// takes two sums one after the other.  A cluster, where each costs several
+// times as much, puts the second together from sums that do not need dh (dh is
+// dh_out + r1 dn - r1 <dn n> n), so a row takes one; the extra products and
+// reads of shared memory made a single CTA slower (8192 x 7168 bf16: 150 us
+// against 132).
+template <bool kF32, int V, int D, int kC>
+__global__ void __maxnreg__(backward_regs(kF32, V))
     norm_residual_backward_kernel(const void* dz, const void* dh_out, const void* h, const void* y, Shape S, Params P,
-                                  void* dh, void* dy, float* __restrict__ dgate, float* __restrict__ part) {
-  extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ RowSum<4, kC> sm4;
-  __shared__ RowSum<1, kC> sm1;
-  constexpr int D = kBackwardStages;
+                                  void* dh, void* dy, float* __restrict__ dgate, float* __restrict__ part, uint32_t* err) {
+  constexpr bool kOneSum = kC > 1;
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ RowSum<kOneSum ? 8 : 4, kC> sm;
+  __shared__ RowSum<1, 1> sm_dot;
+  row_sum_init(sm);
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
   const int col0 = rank * S.cols;
@@ -295,52 +312,74 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 1 : 3)
   long at = src.fetch_at;
 #pragma unroll
   for (int s = 0; s < D - 1; ++s) src.fetch(tensors, 2);
-  // s post_w (g per channel) stays in shared memory, pre_w and the sums in registers
+  // a = s post_w (g per channel) stays in shared memory, the sums in registers,
+  // and so does pre_w where there is room
   const uint32_t a_at = fp8g::smem_u32(dyn) + 4 * D * S.pitch + threadIdx.x * 32;
-  Pair8 pw[V], acc_pre[V] = {}, acc_u[V] = {};
+  const uint32_t pre_at = a_at + V * blockDim.x * 32;
+  Pair8 pre_reg[kOneSum ? 1 : V], acc_pre[V] = {}, acc_u[V] = {};
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    Pair8 a;
-    column_params(P, col0 + 8 * (threadIdx.x + v * blockDim.x), src.in[v], pw[v], a);
+    Pair8 a, pw;
+    column_params(P, col0 + 8 * (threadIdx.x + v * blockDim.x), src.in[v], pw, a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) a.v[i] = mul2(a.v[i], both(P.scale));
     keep8(a_at + v * blockDim.x * 32, a);
+    if constexpr (kOneSum) keep8(pre_at + v * blockDim.x * 32, pw);
+    else pre_reg[v] = pw;
   }
+  auto pre = [&](int v) {
+    if constexpr (kOneSum) return kept8(pre_at + v * blockDim.x * 32);
+    else return pre_reg[v];
+  };
   if constexpr (kC > 1) cluster_sync_all();
+  if (threadIdx.x == 0) fp8g::grid_launch_dependents();  // the kernel that adds the partial rows waits for this one
   const float inv_h = 1.f / static_cast<float>(S.H);
   const bool token = P.gate_kind == FP8G_GATE_TOKEN;
-  int turn4 = 0, turn1 = 0;
-  for (long row = row0; row < S.rows; row += step) {
+  bool gave_up = false;
+  unsigned it = 0;
+  for (long row = row0; row < S.rows; row += step, ++it) {
     src.fetch(tensors, 2);
     cp_wait<D - 1>();
-    Pair8 hv[V], yv[V], g[V];         // g: dz, then dh, then du
-    uint64_t hh = 0, dn = 0, yy = 0;  // h'^2, (dz pre_w) h', y^2
+    Pair8 hv[V], yv[V], g[V];  // g: dz, then dh, then du
+    // h'^2, dn h', y^2 with dn = dz pre_w; and a y dh_out, a y dn, a y h'
+    uint64_t hh = 0, nh = 0, yy = 0, ad = 0, an = 0, ah = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       hv[v] = src.load(0, v), yv[v] = src.load(1, v), g[v] = src.load(2, v);
+      const Pair8 pw = pre(v);
+      Pair8 d = {}, a = {};
+      if constexpr (kOneSum) d = src.load(3, v), a = kept8(a_at + v * blockDim.x * 32);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const uint64_t n = mul2(g[v].v[i], pw.v[i]);
         hh = fma2(hv[v].v[i], hv[v].v[i], hh);
-        dn = fma2(mul2(g[v].v[i], pw[v].v[i]), hv[v].v[i], dn);
+        nh = fma2(n, hv[v].v[i], nh);
         yy = fma2(yv[v].v[i], yv[v].v[i], yy);
+        if constexpr (kOneSum) {
+          const uint64_t ay = mul2(a.v[i], yv[v].v[i]);
+          ad = fma2(ay, d.v[i], ad);
+          an = fma2(ay, n, an);
+          ah = fma2(ay, hv[v].v[i], ah);
+        }
       }
     }
-    float st[4] = {sum2(hh), sum2(dn), sum2(yy), 0.f};
-    row_sum<4, kC>(st, sm4, turn4, rank);
+    float st[kOneSum ? 8 : 4] = {sum2(hh), sum2(nh), sum2(yy)};
+    if constexpr (kOneSum) st[3] = sum2(ad), st[4] = sum2(an), st[5] = sum2(ah);
+    row_sum(st, sm, it, rank, gave_up, err);
+    const float gt = token ? __ldg(P.gate + row) : 1.f;
     const float r1 = rms_factor(st[0], inv_h, P.eps);
     const float r2 = P.post_w ? rms_factor(st[2], inv_h, P.eps) : 1.f;
-    const float gt = token ? __ldg(P.gate + row) : 1.f;
-    const uint64_t rr1 = both(r1), rr2 = both(r2);
-    const uint64_t rm = both(-r1 * (st[1] * r1 * inv_h));  // - r1 <dz pre_w n>
-    uint64_t du_u = 0;                                     // a dh u
+    const float m1 = -r1 * (st[1] * r1 * inv_h);  // - r1 <dn n>, n = h' r1
+    const uint64_t rr1 = both(r1), rr2 = both(r2), rm = both(m1);
+    uint64_t du_u = 0;  // a dh u
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const Pair8 t = src.load(3, v);
+      const Pair8 d = src.load(3, v), pw = pre(v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t n = mul2(hv[v].v[i], rr1);
         acc_pre[v].v[i] = fma2(g[v].v[i], n, acc_pre[v].v[i]);
-        g[v].v[i] = fma2(n, rm, fma2(mul2(g[v].v[i], pw[v].v[i]), rr1, t.v[i]));
+        g[v].v[i] = fma2(n, rm, fma2(mul2(g[v].v[i], pw.v[i]), rr1, d.v[i]));
       }
       if (src.in[v]) put8<kF32>(dh, at + v * src.apart(), g[v]);
       const Pair8 a = kept8(a_at + v * blockDim.x * 32);
@@ -349,17 +388,20 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 1 : 3)
         yv[v].v[i] = mul2(yv[v].v[i], rr2);
         acc_u[v].v[i] = fma2(token ? mul2(g[v].v[i], both(gt)) : g[v].v[i], yv[v].v[i], acc_u[v].v[i]);
         g[v].v[i] = mul2(g[v].v[i], a.v[i]);
-        du_u = fma2(g[v].v[i], yv[v].v[i], du_u);
+        if constexpr (!kOneSum) du_u = fma2(g[v].v[i], yv[v].v[i], du_u);
       }
     }
     src.advance();
-    float m2 = 0.f;  // <du u>
-    if (P.post_w || token) {
-      float dot[1] = {sum2(du_u)};
-      row_sum<1, kC>(dot, sm1, turn1, rank);
-      if (P.post_w) m2 = dot[0] * gt * inv_h;
-      if (dgate && token && rank == 0 && threadIdx.x == 0) dgate[row] = dot[0];
+    float dot = 0.f;
+    if constexpr (kOneSum) {
+      dot = r2 * fmaf(m1 * r1, st[5], fmaf(r1, st[4], st[3]));
+    } else if (P.post_w || token) {
+      float s1[1] = {sum2(du_u)};
+      row_sum(s1, sm_dot, it, rank, gave_up, err);
+      dot = s1[0];
     }
+    const float m2 = P.post_w ? dot * gt * inv_h : 0.f;  // <du u>
+    if (dgate && token && rank == 0 && threadIdx.x == 0) dgate[row] = dot;
     const uint64_t f = both(r2 * gt), um = both(-r2 * m2);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -387,7 +429,7 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 1 : 3)
 }
 
 // Sums of partial rows part[2][P][H] over P.  A CTA takes 32 columns and the
-// partial rows of its blockIdx.y: its 32 warps every 32nd row each, 8 loads
+// partial rows of its blockIdx.y: its 32 warps every 32nd row each, 4 loads
 // at a time, then the warps' sums in warp order (8192 x 7168, 148 partial rows:
 // latency of one or two rounds of loads).  Many partial rows (narrow
 // rows have many CTAs) are summed in two launches: to out[2][gridDim.y][H]
@@ -395,7 +437,7 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 1 : 3)
 constexpr int kSumWarps = 32;
 
 template <bool kLast>
-__global__ void __launch_bounds__(32 * kSumWarps) norm_param_grad_kernel(const float* __restrict__ part, int P, int H, int per,
+__global__ void __launch_bounds__(32 * kSumWarps, 2) norm_param_grad_kernel(const float* __restrict__ part, int P, int H, int per,
                                                               float* __restrict__ out, Params prm, float* dpre,
                                                               float* dpost, float* dgate) {
   __shared__ float s[2][kSumWarps][32];
@@ -403,11 +445,18 @@ __global__ void __launch_bounds__(32 * kSumWarps) norm_param_grad_kernel(const f
   const int col = blockIdx.x * 32 + lane;
   const int p0 = blockIdx.y * per, p1 = min(P, p0 + per);
   float a = 0.f, b = 0.f;
+  fp8g::grid_dependency_wait();  // launched while the kernel that writes part still runs
   if (col < H) {
-#pragma unroll 8
-    for (int p = p0 + w; p < p1; p += kSumWarps) {
-      a += part[static_cast<long>(p) * H + col];
-      b += part[(static_cast<long>(P) + p) * H + col];
+    for (int p = p0 + w; p < p1; p += 4 * kSumWarps) {
+      float x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = p + i * kSumWarps;
+        x[i] = q < p1 ? part[static_cast<long>(q) * H + col] : 0.f;
+        y[i] = q < p1 ? part[(static_cast<long>(P) + q) * H + col] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a += x[i], b += y[i];
     }
   }
   s[0][w][lane] = a;
@@ -443,21 +492,24 @@ struct Plan {
 
 constexpr int kSms = 148;
 constexpr int kSmemPerSm = 224 << 10;  // of 227 KB: the static part takes up to 5 KB where the stages leave more
-// rows up to so many columns get one vector a thread: more, shorter CTAs
+// Rows up to so many columns get one vector a thread, wider ones two: half the
+// warps carry the per-row work (8192 x 4096 bf16 backward 104 us with one vector,
+// 72 with two; 8192 x 3000 forward 45 and 37).
 constexpr int kNarrow = 2048;
 
 // tensors: rows streamed per stage.  The cluster grows until a CTA has at most
-// max_threads and its stages fit the shared memory; as many CTAs per SM as the
+// kMaxThreads and its stages fit the shared memory; as many CTAs per SM as the
 // registers of `sm_threads` threads and the stages allow.
-Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int vecs, int sm_threads) {
+Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int vecs, int sm_threads,
+             int kept_one, int kept_cluster) {
   Plan p{};
   p.vecs = vecs;
   for (p.ctas = 1;; p.ctas *= 2) {
     const int cols = ((H + unit - 1) / unit + p.ctas - 1) / p.ctas * unit;
     p.threads = (cols / 8 + 32 * vecs - 1) / (32 * vecs) * 32;
     p.S = Shape{rows, H, cols, static_cast<uint32_t>(p.threads * vecs * 8 * esz)};
-    p.smem = tensors * stages * static_cast<int>(p.S.pitch) + 32 * vecs * p.threads;
-    if (p.ctas == 4 || (p.threads <= max_threads(vecs) && p.smem <= kSmemPerSm)) break;
+    p.smem = tensors * stages * static_cast<int>(p.S.pitch) + (p.ctas == 1 ? kept_one : kept_cluster) * p.threads;
+    if (p.ctas == 4 || (p.threads <= std::min(kMaxThreads, sm_threads) && p.smem <= kSmemPerSm)) break;
   }
   const int per_sm = std::max(1, std::min({32, sm_threads / p.threads, kSmemPerSm / p.smem}));
   // no more clusters than rows, and no more than it takes for all to have the
@@ -474,12 +526,14 @@ Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int ve
 Plan forward_plan(int rows, int H, int dtype) {
   const bool f32 = dtype == FP8G_IN_F32;
   const int vecs = H <= kNarrow ? 1 : 2;
-  return plan_of(rows, H, f32 ? 4 : 2, 2, forward_stages(f32, vecs), H % 128 == 0 ? 128 : 8, vecs, 1024);
+  return plan_of(rows, H, f32 ? 4 : 2, 2, forward_stages(f32, vecs), H % 128 == 0 ? 128 : 8, vecs, threads_at(64), 32 * vecs, 32 * vecs);
 }
 
 Plan backward_plan(int rows, int H, int dtype) {
   const int vecs = H <= kNarrow ? 1 : 2;
-  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 4, kBackwardStages, 8, vecs, vecs == 1 ? 768 : 512);
+  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 4, backward_stages(dtype == FP8G_IN_F32, H), 8, vecs,
+                 threads_at(backward_regs(dtype == FP8G_IN_F32, vecs)),
+                 32 * vecs, 64 * vecs);
 }
 
 // Launches the kernel for the plan's cluster size.
@@ -533,9 +587,11 @@ extern "C" int fp8g_norm_residual(const void* y, const void* h, int dtype, int r
   if (!aligned(y, 16) || !aligned(h, 16) || !aligned(h_out, 16) || !aligned(z, 16) || !aligned(q, 16) ||
       (q && !aligned(sa, 16)) || !params_aligned(post_w, gate, gate_kind, pre_w))
     return FP8G_ERR_MISALIGNED;
+  uint32_t* err = fp8g::device_error_word();
+  if (!err) return FP8G_ERR_CUDA;
   const Plan p = forward_plan(rows, H, dtype);
   const Params P{post_w, gate, pre_w, gate_kind, scale, eps};
-  auto go = [&](auto kernel) { return launch(p, kernel, stream, y, h, p.S, P, h_out, z, q, sa, ld_sa); };
+  auto go = [&](auto kernel) { return launch(p, kernel, stream, y, h, p.S, P, h_out, z, q, sa, ld_sa, err); };
   auto by_split = [&](auto narrow, auto one, auto two) { return p.vecs == 1 ? go(narrow) : p.ctas == 1 ? go(one) : go(two); };
   cudaError_t e;
   if (dtype == FP8G_IN_F32)
@@ -581,21 +637,23 @@ extern "C" int fp8g_norm_residual_backward(const void* dz, const void* dh_out, c
       !params_aligned(post_w, gate, gate_kind, pre_w))
     return FP8G_ERR_MISALIGNED;
   if (rows == 0 && !params) return FP8G_OK;
+  uint32_t* err = fp8g::device_error_word();
+  if (!err) return FP8G_ERR_CUDA;
   const Plan p = backward_plan(rows, H, dtype);
   const Params P{post_w, gate, pre_w, gate_kind, scale, eps};
   float* part = params ? static_cast<float*>(workspace) : nullptr;
   if (rows > 0) {
-    auto go = [&](auto kernel) { return launch(p, kernel, stream, dz, dh_out, h_out, y, p.S, P, dh, dy, dgate, part); };
+    auto go = [&](auto kernel) { return launch(p, kernel, stream, dz, dh_out, h_out, y, p.S, P, dh, dy, dgate, part, err); };
     cudaError_t e;
-    if (dtype == FP8G_IN_F32)
-      e = p.vecs == 1   ? go(norm_residual_backward_kernel<true, 1, 1>)
-          : p.ctas == 1 ? go(norm_residual_backward_kernel<true, 2, 1>)
-          : p.ctas == 2 ? go(norm_residual_backward_kernel<true, 2, 2>)
-                        : go(norm_residual_backward_kernel<true, 2, 4>);
-    else
-      e = p.vecs == 1   ? go(norm_residual_backward_kernel<false, 1, 1>)
-          : p.ctas == 1 ? go(norm_residual_backward_kernel<false, 2, 1>)
-                        : go(norm_residual_backward_kernel<false, 2, 2>);
+    if (dtype == FP8G_IN_F32)  // 1 CTA up to 5600 columns, 2 up to 11264
+      e = p.vecs == 1   ? go(norm_residual_backward_kernel<true, 1, 2, 1>)
+          : p.ctas == 1 ? go(norm_residual_backward_kernel<true, 2, 2, 1>)
+          : p.ctas == 2 ? go(norm_residual_backward_kernel<true, 2, 2, 2>)
+                        : go(norm_residual_backward_kernel<true, 2, 2, 4>);
+    else  // 1 CTA up to 8192 columns, 2 above
+      e = p.vecs == 1   ? go(norm_residual_backward_kernel<false, 1, 3, 1>)
+          : p.ctas == 1 ? go(norm_residual_backward_kernel<false, 2, 3, 1>)
+                        : go(norm_residual_backward_kernel<false, 2, 2, 2>);
     if (e != cudaSuccess) {
       (void)cudaGetLastError();
       return FP8G_ERR_CUDA;
@@ -604,15 +662,22 @@ extern "C" int fp8g_norm_residual_backward(const void* dz, const void* dh_out, c
   if (params) {
     const unsigned groups = (H + 31) / 32;
     int n = rows > 0 ? static_cast<int>(p.clusters) : 0;
+    cudaError_t e = cudaSuccess;
     if (n > kOneLaunch) {
       const int sums = (n + kPartsPerSum - 1) / kPartsPerSum;
       float* out = part + 2L * n * H;
-      norm_param_grad_kernel<false><<<dim3(groups, sums), 32 * kSumWarps, 0, stream>>>(part, n, H, kPartsPerSum, out, P, nullptr, nullptr,
-                                                                            nullptr);
+      e = fp8g::rows::launch_behind(dim3(groups, sums), 32 * kSumWarps, stream, norm_param_grad_kernel<false>, part, n, H,
+                                    kPartsPerSum, out, P, nullptr, nullptr, nullptr);
       part = out;
       n = sums;
     }
-    norm_param_grad_kernel<true><<<groups, 32 * kSumWarps, 0, stream>>>(part, n, H, n, nullptr, P, dpre_w, dpost_w, dgate);
+    if (e == cudaSuccess)
+      e = fp8g::rows::launch_behind(dim3(groups), 32 * kSumWarps, stream, norm_param_grad_kernel<true>, part, n, H, n,
+                                    nullptr, P, dpre_w, dpost_w, dgate);
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      return FP8G_ERR_CUDA;
+    }
   }
   if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
   return FP8G_OK;
