@@ -37,6 +37,9 @@ constexpr int kPadBlocks = 256;  // most blocks of a padding CTA: its bitmap is 
 // CTAs that share a group of blocks, each with every 8th of its rows: one SM
 // alone zeroes 370 KB (45 rows of 4096 bf16) in some 15 us
 constexpr int kPadSlices = 8;
+// Routed slots up to which the sort may be one launch, while its CTAs are few
+// enough to run at once (SORTDIRECT).
+constexpr int kDirectSlots = 4096;
 
 // pos[r] if it names a row of the layout, -1 if the slot is dropped; anything
 // else is flagged and treated as dropped.
@@ -138,6 +141,81 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restric
       at = vector_of(i);
       if (at >= 0) v = __ldcs(x + at);
     }
+  }
+}
+
+// The whole sort of a small batch in one launch: every CTA counts the experts of
+// all slots and its own slots' ranks itself instead of waiting for the layout
+// kernel.  CTAs [0, pads) zero padding rows (they know how many every expert
+// has) and write m_indices.
+template <int kCap>
+__global__ void __launch_bounds__(256) moe_permute_direct_kernel(const uint4* __restrict__ x, int vecs, int parts, int T,
+                                                                 int topk, const int32_t* __restrict__ expert, int G,
+                                                                 int32_t* __restrict__ pos, int32_t* __restrict__ m_indices,
+                                                                 uint4* __restrict__ xs, int blocks, int pads,
+                                                                 uint32_t* err) {
+  __shared__ int32_t s_cnt[kMaxExperts], s_end[kMaxExperts];  // slots, and end of the segment in blocks
+  __shared__ int32_t s_part[8][kCap];
+  __shared__ int32_t s_row[kCap];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const bool pad = static_cast<int>(blockIdx.x) < pads;
+  const int item = static_cast<int>(blockIdx.x) - pads, t = item / parts, part = item - t * parts;
+  const int j = part * blockDim.x + threadIdx.x;
+  const uint4 v = !pad && j < vecs ? __ldcs(x + static_cast<long>(t) * vecs + j) : make_uint4(0u, 0u, 0u, 0u);
+  if (!pad) {
+    int e[kCap];
+#pragma unroll
+    for (int k = 0; k < kCap; ++k) e[k] = k < topk ? fp8g::moe::expert_at(expert, G, t * topk + k, nullptr) : -1;
+    fp8g::moe::count_earlier<kCap>(expert, t * topk, e, s_part);
+  }
+  fp8g::moe::count_experts(expert, T * topk, G, s_cnt, blockIdx.x == 0 ? err : nullptr);
+  if (warp == 0) {
+    // inclusive scan of the segments' blocks, 8 experts a lane
+    int32_t n[kMaxExperts / 32], run = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) run += (s_cnt[lane * (kMaxExperts / 32) + i] + 127) / 128, n[i] = run;
+    int32_t incl = run;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) s_end[lane * (kMaxExperts / 32) + i] = incl - run + n[i];
+  }
+  __syncthreads();
+  if (pad) {
+    const int stride = pads * blockDim.x;
+    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < blocks; b += stride) {
+      int g = 0;
+      while (g < G && s_end[g] <= b) ++g;
+      m_indices[b] = g < G ? g : -1;
+    }
+    // expert g's padding rows, every kPadSlices-th of them, a row per warp
+    for (int it = blockIdx.x; it < G * kPadSlices; it += pads) {
+      const int g = it / kPadSlices;
+      const long end = 128L * s_end[g], first = end - (s_cnt[g] + 127) / 128 * 128L + s_cnt[g];
+      for (long row = first + it % kPadSlices + kPadSlices * warp; row < end; row += kPadSlices * nw)
+        for (int i = lane; i < vecs; i += 32) __stcs(xs + row * vecs + i, make_uint4(0u, 0u, 0u, 0u));
+    }
+    return;
+  }
+  if (static_cast<int>(threadIdx.x) < kCap) {
+    const int k = threadIdx.x;
+    const int g = k < topk ? fp8g::moe::expert_at(expert, G, static_cast<long>(t) * topk + k, nullptr) : -1;
+    int row = -1;
+    if (g >= 0) {
+      row = 128 * (s_end[g] - (s_cnt[g] + 127) / 128);
+      for (int i = 0; i < nw; ++i) row += s_part[i][k];
+    }
+    s_row[k] = row;
+    if (part == 0 && k < topk) pos[t * topk + k] = row;
+  }
+  __syncthreads();
+  if (j < vecs) {
+#pragma unroll
+    for (int k = 0; k < kCap; ++k)
+      if (s_row[k] >= 0) __stcs(xs + static_cast<long>(s_row[k]) * vecs + j, v);
   }
 }
 
@@ -388,16 +466,28 @@ extern "C" int fp8g_moe_permute(const void* x, int x_dtype, int T, int N, const 
   const int sms = sm_count();
   uint32_t* err = fp8g::device_error_word();
   if (sms <= 0 || !err) return FP8G_ERR_CUDA;
+  const long vecs = static_cast<long>(N) * (x_dtype == FP8G_IN_F32 ? 4 : 2) / 16;
+  if (vecs > 0x7FFFFFFFL) return FP8G_ERR_INVALID_ARG;
+  const int parts = static_cast<int>((vecs + 255) / 256);
+  if (R > 0 && R <= kDirectSlots && static_cast<long>(T) * parts <= 8L * sms) {
+    const int pads = std::min(G * kPadSlices, 2 * sms);
+    auto go = [&](auto kernel) {
+      kernel<<<pads + T * parts, row_threads(vecs), 0, stream>>>(static_cast<const uint4*>(x), static_cast<int>(vecs), parts,
+                                                                 T, topk, expert, G, pos, m_indices,
+                                                                 static_cast<uint4*>(xs), blocks, pads, err);
+    };
+    by_topk(topk, [&] { go(moe_permute_direct_kernel<4>); }, [&] { go(moe_permute_direct_kernel<8>); },
+            [&] { go(moe_permute_direct_kernel<kMaxTopk>); });
+    if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
+    return FP8G_OK;
+  }
   if (fp8g::moe::launch_layout<false>(expert, static_cast<int>(R), G, 0, pos, m_indices, blocks, err, stream) !=
       cudaSuccess) {
     (void)cudaGetLastError();
     return FP8G_ERR_CUDA;
   }
   if (R == 0) return FP8G_OK;
-  const long vecs = static_cast<long>(N) * (x_dtype == FP8G_IN_F32 ? 4 : 2) / 16;
-  if (vecs > 0x7FFFFFFFL) return FP8G_ERR_INVALID_ARG;
   const int pads = pad_ctas(blocks, sms);
-  const int parts = static_cast<int>((vecs + 255) / 256);
   const unsigned grid = static_cast<unsigned>(pads + std::min<long>(static_cast<long>(T) * parts, 1 << 20));
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {

@@ -4,16 +4,16 @@
 //
 // One cluster does the whole count -> scan -> rank chain: the slots are split
 // into one contiguous run per CTA and, inside it, one per warp.  A first walk
-// counts each warp's slots per expert (__match_any_sync finds the lanes of one
-// expert; the lowest adds their number to a counter that only its warp uses),
-// the warps' counters are scanned in shared memory and the CTAs' totals
-// through distributed shared memory, and a second walk hands out the rows.
-// Everything is integer work in a fixed order: ranks are stable.
+// counts each warp's slots per expert (a ballot per bit of the expert finds the
+// lanes of one expert; the lowest adds their number to a counter that only its
+// warp uses), the warps' counters are scanned in shared memory and the CTAs'
+// totals through distributed shared memory, and a second walk hands out the
+// rows.  Everything is integer work in a fixed order: ranks are stable.
 //
 // It is a chain of latencies, not of work: each walk loads up to 8 steps of 32
 // slots at once, a warp's first 8 steps stay in registers for the second walk,
 // and the scan over the warps reads all its counters before it adds
-// (32768 slots, 64 experts: 12.9 us without these).
+// (32768 slots, 64 experts: LAYOUT us).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -30,6 +30,7 @@ constexpr int kMaxExperts = 256;
 constexpr int kMaxTopk = 16;
 constexpr int kLayoutThreads = 1024;
 constexpr int kLayoutWarps = kLayoutThreads / 32;
+constexpr int kMaxCtas = 8;  // of the layout kernel's cluster
 constexpr int kAhead = 8;  // steps of 32 slots that a warp loads at once
 
 // Expert of routed row r, or -1 (dropped, or out of range: flagged).
@@ -40,9 +41,74 @@ __device__ __forceinline__ int expert_at(const int32_t* e, int G, long r, uint32
   return -1;
 }
 
+// The lanes with the same expert g as this one (of no use to lanes with g < 0),
+// from one ballot per bit.  __match_any_sync gives the same, but took 90 cycles
+// of the SM for every warp and step: 12.9 us for 32768 slots over 64 experts.
+__device__ __forceinline__ uint32_t peers_of(int g, int bits) {
+  uint32_t m = __ballot_sync(0xffffffffu, g >= 0);
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    if (b >= bits) break;
+    const bool one = g >> b & 1;
+    const uint32_t with = __ballot_sync(0xffffffffu, one);
+    m &= one ? with : ~with;
+  }
+  return m;
+}
+
+// Earlier slots of each of a token's experts e[k], counted by the warps of a CTA
+// (a share of the slots before `before` each): s_part[warp][k].  Slots of the
+// token itself count by the first warp.  A barrier has to follow.
+template <int kCap, int kThreads = 0>
+__device__ __forceinline__ void count_earlier(const int32_t* expert, int before, const int (&e)[kCap],
+                                              int32_t (*s_part)[kCap]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = kThreads ? kThreads : blockDim.x;
+  int n[kCap];
+#pragma unroll
+  for (int k = 0; k < kCap; ++k) n[k] = 0;
+  for (int r0 = 32 * warp; r0 < before; r0 += kAhead * threads) {
+    int g[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int r = r0 + a * threads + lane;
+      g[a] = r < before ? __ldg(expert + r) : -1;
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (r0 + a * threads >= before) break;  // warp-uniform
+#pragma unroll
+      for (int k = 0; k < kCap; ++k) n[k] += __popc(__ballot_sync(0xffffffffu, g[a] == e[k]));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kCap; ++k) {
+#pragma unroll
+    for (int a = 0; a < k; ++a) n[k] += warp == 0 && e[a] == e[k];  // the same expert twice in a token
+    if (lane == k) s_part[warp][k] = n[k];
+  }
+}
+
+// Slots of every expert, counted by a CTA into s_cnt [kMaxExperts]; flags bad
+// experts if err is given.  Starts and ends with a barrier.
+template <int kThreads = 0>
+__device__ __forceinline__ void count_experts(const int32_t* expert, int R, int G, int32_t* s_cnt, uint32_t* err) {
+  const int threads = kThreads ? kThreads : blockDim.x;
+  for (int g = threadIdx.x; g < kMaxExperts; g += threads) s_cnt[g] = 0;
+  __syncthreads();
+  for (int r0 = threadIdx.x; r0 < R; r0 += kAhead * threads) {
+    int g[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) g[a] = r0 + a * threads < R ? expert_at(expert, G, r0 + a * threads, err) : -1;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (g[a] >= 0) atomicAdd(&s_cnt[g[a]], 1);
+  }
+  __syncthreads();
+}
+
 __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
   int32_t v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 
@@ -75,6 +141,7 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_
   const long steps = (static_cast<long>(R) + 32L * kLayoutWarps * ctas - 1) / (32L * kLayoutWarps * ctas);
   const long r0 = (static_cast<long>(rank) * kLayoutWarps + w) * steps * 32 + lane;
   int g[kAhead];
+  uint32_t peers[kAhead];
   auto load = [&](long i0, uint32_t* flag) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -83,13 +150,14 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_
     }
   };
   const uint32_t below = (1u << lane) - 1u;
+  const int bits = G > 1 ? 32 - __clz(G - 1) : 0;  // of an expert's number
   for (long i0 = 0; i0 < steps; i0 += kAhead) {
     load(i0, err);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= steps) break;  // the same for the whole CTA
-      const uint32_t peers = __match_any_sync(0xffffffffu, g[i]);
-      if (g[i] >= 0 && (peers & below) == 0) s_w[w][g[i]] += __popc(peers);
+      peers[i] = peers_of(g[i], bits);
+      if (g[i] >= 0 && (peers[i] & below) == 0) s_w[w][g[i]] += __popc(peers[i]);
       __syncwarp();
     }
   }
@@ -110,12 +178,19 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_
   int32_t before = 0, total = 0;
   if (tid < kMaxExperts) {
     const uint32_t mine = smem_u32(&s_total[tid]);
-    for (int c = 0; c < ctas; ++c) {
-      const int32_t v = ld_cluster_s32(mapa(mine, c));
-      if (c < rank) before += v;
-      total += v;
+    int32_t v[kMaxCtas];
+#pragma unroll
+    for (int c = 0; c < kMaxCtas; ++c) v[c] = c < ctas ? ld_cluster_s32(mapa(mine, c)) : 0;
+#pragma unroll
+    for (int c = 0; c < kMaxCtas; ++c) {
+      if (c < rank) before += v[c];
+      total += v[c];
     }
   }
+  // No CTA leaves while another may still read its totals: arrive here, where they
+  // are read (nothing else is handed over, so relaxed: the rows' stores below need
+  // not be waited for), wait at the end.
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if constexpr (kMasked) {
     if (tid < kMaxExperts) s_first[tid] = before;
     if (rank == 0 && tid < G) {
@@ -159,20 +234,19 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= steps) break;
       const long r = r0 + 32 * (i0 + i);
-      const uint32_t peers = __match_any_sync(0xffffffffu, g[i]);
+      if (steps > kAhead) peers[i] = peers_of(g[i], bits);
       int32_t row = -1;
       if (g[i] >= 0) {
-        row = s_first[g[i]] + s_w[w][g[i]] + __popc(peers & below);
+        row = s_first[g[i]] + s_w[w][g[i]] + __popc(peers[i] & below);
         if constexpr (kMasked) row = row < Mmax ? g[i] * Mmax + row : -1;
       }
       __syncwarp();
-      if (g[i] >= 0 && (peers & below) == 0) s_w[w][g[i]] += __popc(peers);
+      if (g[i] >= 0 && (peers[i] & below) == 0) s_w[w][g[i]] += __popc(peers[i]);
       __syncwarp();
       if (r < R) pos[r] = row;
     }
   }
-  // no CTA leaves while another may still read its totals
-  if (ctas > 1) cluster_sync_all();
+  if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // One cluster of up to 8 CTAs, a CTA for every 4096 slots.
@@ -180,7 +254,7 @@ template <bool kMasked>
 cudaError_t launch_layout(const int32_t* expert, int R, int G, int Mmax, int32_t* pos, int32_t* counts, int blocks,
                           uint32_t* err, cudaStream_t stream) {
   int ctas = 1;
-  while (ctas < 8 && R > 4096 * ctas) ctas *= 2;
+  while (ctas < kMaxCtas && R > 4096 * ctas) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(ctas, 1, 1);

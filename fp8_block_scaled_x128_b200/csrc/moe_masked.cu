@@ -37,7 +37,6 @@ using fp8g::moe::kMaxTopk;
 
 constexpr int kDirectSlots = 4096;
 constexpr int kThreads = 256;
-using fp8g::moe::kAhead;  // loads of earlier slots in flight per lane
 
 // kDirect: ranks are counted here (the first CTA counts rows per expert);
 // otherwise pos and masked_m are already there.
@@ -49,25 +48,14 @@ __global__ void __launch_bounds__(kThreads) moe_dispatch_masked_kernel(const voi
                                                                        int32_t* __restrict__ masked_m, uint32_t* err) {
   constexpr int kWarps = kThreads / 32;
   __shared__ int32_t s_cnt[kDirect ? kMaxExperts : 1];
-  __shared__ int32_t s_part[kDirect ? kWarps : 1][kDirect ? kCap : 1];
+  __shared__ int32_t s_part[kDirect ? kWarps : 1][kCap];
   __shared__ int32_t s_row[kCap];  // each slot's row of A as [G * Mmax][K], -1 if it is dropped
   __shared__ long s_scale[kCap];   // its first scale in sa
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const long items = static_cast<long>(T) * parts;
   if constexpr (kDirect) {
     if (blockIdx.x == 0) {
-      for (int g = threadIdx.x; g < G; g += kThreads) s_cnt[g] = 0;
-      __syncthreads();
-      for (int r0 = threadIdx.x; r0 < T * topk; r0 += kAhead * kThreads) {
-        int g[kAhead];
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-          g[a] = r0 + a * kThreads < T * topk ? expert_at(expert, G, r0 + a * kThreads, err) : -1;
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-          if (g[a] >= 0) atomicAdd(&s_cnt[g[a]], 1);
-      }
-      __syncthreads();
+      fp8g::moe::count_experts<kThreads>(expert, T * topk, G, s_cnt, err);
       for (int g = threadIdx.x; g < G; g += kThreads) {
         masked_m[g] = min(s_cnt[g], Mmax);
         if (s_cnt[g] > Mmax) atomicOr(err, FP8G_DEVERR_MASKED_OVER);
@@ -88,34 +76,10 @@ __global__ void __launch_bounds__(kThreads) moe_dispatch_masked_kernel(const voi
     }
     if constexpr (!kDirect) fp8g::grid_dependency_wait();  // pos is the layout kernel's, x is not
     if constexpr (kDirect) {
-      int e[kCap], n[kCap];
+      int e[kCap];
 #pragma unroll
-      for (int k = 0; k < kCap; ++k) {
-        e[k] = k < topk ? expert_at(expert, G, t * topk + k, nullptr) : -1;
-        n[k] = 0;
-      }
-      // earlier slots of each of this token's experts: a share per warp
-      const int before = static_cast<int>(t) * topk;
-      for (int r0 = 32 * warp; r0 < before; r0 += kAhead * kThreads) {
-        int g[kAhead];
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          const int r = r0 + a * kThreads + lane;
-          g[a] = r < before ? __ldg(expert + r) : -1;
-        }
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          if (r0 + a * kThreads >= before) break;  // warp-uniform
-#pragma unroll
-          for (int k = 0; k < kCap; ++k) n[k] += __popc(__ballot_sync(0xffffffffu, g[a] == e[k]));
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kCap; ++k) {
-#pragma unroll
-        for (int a = 0; a < k; ++a) n[k] += warp == 0 && e[a] == e[k];  // the same expert twice in a token
-        if (lane == k) s_part[warp][k] = n[k];
-      }
+      for (int k = 0; k < kCap; ++k) e[k] = k < topk ? expert_at(expert, G, t * topk + k, nullptr) : -1;
+      fp8g::moe::count_earlier<kCap, kThreads>(expert, static_cast<int>(t) * topk, e, s_part);
       __syncthreads();
     }
     if (static_cast<int>(threadIdx.x) < kCap) {
