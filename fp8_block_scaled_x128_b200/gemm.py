@@ -345,28 +345,24 @@ def moe_combine(D, pos, w, T, topk, out=None, stream=None):
     return out
 
 
-def _shaped(t, dt, shape, name):
-    """t, if it is a contiguous CUDA tensor of this type and shape (a tuple)."""
+def _operand(t, dt, shape, dev, name):
+    """t, if it is a contiguous tensor of this type and shape (a tuple) on dev.
+    One check per operand, kept short: these calls are made per layer and
+    decoded token."""
     if t.dtype != dt or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous CUDA tensor of {dt} {tuple(shape)}, got {t.dtype} "
                         f"{tuple(t.shape)} on {t.device}")
+    if t.device != dev:
+        raise ValueError(f"all operands must be on one device: {name} is on {t.device}, expected {dev}")
     return t
 
 
 def _rows(t, name):
+    """The device of t, if it is a contiguous 2-D CUDA tensor of activations."""
     if t.dtype not in _IN_DTYPE or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous 2-D CUDA tensor of bfloat16 or float32, got {t.dtype} "
                         f"{tuple(t.shape)} on {t.device}")
-    return t
-
-
-def _all_on(dev, names, *tensors):
-    """Refuses tensors on another device than dev (None stands for a missing one).
-    These calls are made once per layer and decoded token: the checks are kept
-    short, a dict of every operand cost 2 us a call."""
-    for i, t in enumerate(tensors):
-        if t is not None and t.device != dev:
-            raise ValueError(f"all operands must be on one device: {names.split()[i]} is on {t.device}, expected {dev}")
+    return t.device
 
 
 # the raw handle of a device's current stream; without the Stream object of
@@ -412,13 +408,11 @@ def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
     row of D seen as [G*Mmax, N], for moe_combine; slots past an expert's Mmax
     rows are dropped and flagged (DEVERR_MASKED_OVER).  Rows behind masked_m
     are not written.  `out` may pass those four tensors to reuse them."""
-    _rows(x, "x")
+    dev = _rows(x, "x")
     T, K = x.shape
     topk, G, Mmax = int(topk), int(G), int(Mmax)
     R = T * topk
-    _shaped(expert, torch.int32, (R,), "expert")
-    dev = x.device
-    _all_on(dev, "expert", expert)
+    _operand(expert, torch.int32, (R,), dev, "expert")
     with _On(dev, stream) as raw:
         if out is None:
             ld = (Mmax + 3) // 4 * 4
@@ -426,10 +420,9 @@ def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
                    torch.empty((G, K // 128, ld), dtype=torch.float32, device=dev),
                    torch.empty(R, dtype=torch.int32, device=dev), torch.empty(G, dtype=torch.int32, device=dev))
         A, sa, pos, masked_m = out
-        _shaped(A, torch.uint8, (G, Mmax, K), "A")
-        _shaped(sa, torch.float32, (G, K // 128, sa.shape[-1]), "sa")
-        _shaped(pos, torch.int32, (R,), "pos"), _shaped(masked_m, torch.int32, (G,), "masked_m")
-        _all_on(dev, "A sa pos masked_m", A, sa, pos, masked_m)
+        _operand(A, torch.uint8, (G, Mmax, K), dev, "A")
+        _operand(sa, torch.float32, (G, K // 128, sa.shape[-1]), dev, "sa")
+        _operand(pos, torch.int32, (R,), dev, "pos"), _operand(masked_m, torch.int32, (G,), dev, "masked_m")
         _check(lib.fp8g_moe_dispatch_masked(x.data_ptr(), _IN_DTYPE[x.dtype], T, K, expert.data_ptr(), topk, G, Mmax,
                                             A.data_ptr(), sa.data_ptr(), sa.shape[-1], pos.data_ptr(),
                                             masked_m.data_ptr(), raw), "fp8g_moe_dispatch_masked")
@@ -442,22 +435,19 @@ def moe_permute(x, expert, topk, G, blocks=None, out=None, stream=None):
     [blocks*128, N] of x's type, pos [T*topk] int32, m_indices [blocks] int32).
     Padding rows of a segment are zero; unused blocks are not written.  `out`
     may pass those three tensors to reuse them."""
-    _rows(x, "x")
+    dev = _rows(x, "x")
     T, N = x.shape
     topk, G = int(topk), int(G)
     R = T * topk
-    _shaped(expert, torch.int32, (R,), "expert")
+    _operand(expert, torch.int32, (R,), dev, "expert")
     nb = moe_blocks(T, topk, G) if blocks is None else int(blocks)
-    dev = x.device
-    _all_on(dev, "expert", expert)
     with _On(dev, stream) as raw:
         if out is None:
             out = (torch.empty((nb * 128, N), dtype=x.dtype, device=dev),
                    torch.empty(R, dtype=torch.int32, device=dev), torch.empty(nb, dtype=torch.int32, device=dev))
         xs, pos, mi = out
-        _shaped(xs, x.dtype, (nb * 128, N), "xs")
-        _shaped(pos, torch.int32, (R,), "pos"), _shaped(mi, torch.int32, (nb,), "m_indices")
-        _all_on(dev, "xs pos m_indices", xs, pos, mi)
+        _operand(xs, x.dtype, (nb * 128, N), dev, "xs")
+        _operand(pos, torch.int32, (R,), dev, "pos"), _operand(mi, torch.int32, (nb,), dev, "m_indices")
         _check(lib.fp8g_moe_permute(x.data_ptr(), _IN_DTYPE[x.dtype], T, N, expert.data_ptr(), topk, G, nb,
                                     xs.data_ptr(), pos.data_ptr(), mi.data_ptr(), raw), "fp8g_moe_permute")
     return xs, pos, mi
@@ -467,17 +457,14 @@ def moe_permute_backward(dxs, pos, T, topk, out=None, stream=None):
     """Gradient of moe_permute (and of moe_dispatch, its quantisation taken as
     the identity): dx [T, N] = sum over a token's slots of dxs[pos] (FP32 in
     slot order, rounded once).  dxs [blocks*128, N] bfloat16 or float32."""
-    _rows(dxs, "dxs")
+    dev = _rows(dxs, "dxs")
     M, N = dxs.shape
     T, topk = int(T), int(topk)
     _layout_rows(M, "dxs")
-    _shaped(pos, torch.int32, (T * topk,), "pos")
-    dev = dxs.device
-    _all_on(dev, "pos", pos)
+    _operand(pos, torch.int32, (T * topk,), dev, "pos")
     with _On(dev, stream) as raw:
         dx = torch.empty((T, N), dtype=dxs.dtype, device=dev) if out is None else out
-        _shaped(dx, dxs.dtype, (T, N), "out")
-        _all_on(dev, "out", dx)
+        _operand(dx, dxs.dtype, (T, N), dev, "out")
         _check(lib.fp8g_moe_permute_backward(dxs.data_ptr(), _IN_DTYPE[dxs.dtype], M // 128, N, pos.data_ptr(), T,
                                              topk, dx.data_ptr(), raw), "fp8g_moe_permute_backward")
     return dx
@@ -500,11 +487,10 @@ def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, str
     _dev(D, torch.bfloat16, "D")
     M, N = D.shape
     _layout_rows(M, "D")
-    _shaped(dout, torch.bfloat16, (T, N), "dout"), _shaped(pos, torch.int32, (T * topk,), "pos")
+    dev = D.device
+    _operand(dout, torch.bfloat16, (T, N), dev, "dout"), _operand(pos, torch.int32, (T * topk,), dev, "pos")
     if w is not None:
-        _shaped(w, torch.float32, (T * topk,), "w")
-    dev = dout.device
-    _all_on(dev, "D pos w", D, pos, w)
+        _operand(w, torch.float32, (T * topk,), dev, "w")
     with _On(dev, stream) as raw:
         if out is None:
             dw = None if w is None else torch.empty(T * topk, dtype=torch.float32, device=dev)
@@ -516,15 +502,14 @@ def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, str
         q = sa = dD = None
         if quantize:
             q, sa, dw = out
-            _shaped(q, torch.uint8, (M, N), "q"), _shaped(sa, torch.float32, (N // 128, sa.shape[-1]), "sa")
+            _operand(q, torch.uint8, (M, N), dev, "q"), _operand(sa, torch.float32, (N // 128, sa.shape[-1]), dev, "sa")
         else:
             dD, dw = out
-            _shaped(dD, torch.bfloat16, (M, N), "dD")
+            _operand(dD, torch.bfloat16, (M, N), dev, "dD")
         if (dw is None) != (w is None):
             raise ValueError("dw: an output exactly if w is given")
         if dw is not None:
-            _shaped(dw, torch.float32, (T * topk,), "dw")
-        _all_on(dev, "dD q sa dw", dD, q, sa, dw)
+            _operand(dw, torch.float32, (T * topk,), dev, "dw")
         _check(lib.fp8g_moe_combine_backward(dout.data_ptr(), D.data_ptr(), N, pos.data_ptr(), _addr(w), T, topk,
                                              M // 128, _addr(dD), _addr(q), _addr(sa),
                                              0 if sa is None else sa.shape[-1], _addr(dw), raw),
@@ -534,17 +519,17 @@ def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, str
 
 def _norm_params(y, post_weight, gate, pre_weight):
     """Checks the parameters of rows y; the kind of the gate."""
-    rows, H = y.shape
+    (rows, H), dev = y.shape, y.device
     if post_weight is not None:
-        _shaped(post_weight, torch.float32, (H,), "post_weight")
+        _operand(post_weight, torch.float32, (H,), dev, "post_weight")
     if pre_weight is not None:
-        _shaped(pre_weight, torch.float32, (H,), "pre_weight")
+        _operand(pre_weight, torch.float32, (H,), dev, "pre_weight")
     if gate is None:
         return 0
     if gate.dim() == 1:
-        _shaped(gate, torch.float32, (H,), "gate")
+        _operand(gate, torch.float32, (H,), dev, "gate")
         return 1
-    _shaped(gate, torch.float32, (rows, 1), "gate")
+    _operand(gate, torch.float32, (rows, 1), dev, "gate")
     return 2
 
 
@@ -558,13 +543,11 @@ def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=
     post_weight, pre_weight [H] float32 (post_weight None: no post-norm,
     pre_weight None: ones); gate float32 [H] (per channel) or [rows, 1] (per
     token).  `out` may pass the returned tensors; h_out may be h, z may be y."""
-    _rows(y, "y")
+    dev = _rows(y, "y")
     rows, H = y.shape
     if h is not None:
-        _shaped(h, y.dtype, (rows, H), "h")
+        _operand(h, y.dtype, (rows, H), dev, "h")
     kind = _norm_params(y, post_weight, gate, pre_weight)
-    dev = y.device
-    _all_on(dev, "h post_weight gate pre_weight", h, post_weight, gate, pre_weight)
     with _On(dev, stream) as raw:
         if out is None:
             if quantize:
@@ -575,12 +558,11 @@ def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=
         z = q = sa = None
         if quantize:
             h_out, q, sa = out
-            _shaped(q, torch.uint8, (rows, H), "q"), _shaped(sa, torch.float32, (H // 128, sa.shape[-1]), "sa")
+            _operand(q, torch.uint8, (rows, H), dev, "q"), _operand(sa, torch.float32, (H // 128, sa.shape[-1]), dev, "sa")
         else:
             h_out, z = out
-            _shaped(z, y.dtype, (rows, H), "z")
-        _shaped(h_out, y.dtype, (rows, H), "h_out")
-        _all_on(dev, "h_out z q sa", h_out, z, q, sa)
+            _operand(z, y.dtype, (rows, H), dev, "z")
+        _operand(h_out, y.dtype, (rows, H), dev, "h_out")
         _check(lib.fp8g_norm_residual(y.data_ptr(), _addr(h), _IN_DTYPE[y.dtype], rows, H, _addr(post_weight),
                                       _addr(gate), kind, scale, _addr(pre_weight), eps, h_out.data_ptr(), _addr(z),
                                       _addr(q), _addr(sa), 0 if sa is None else sa.shape[-1], raw),
@@ -596,33 +578,30 @@ def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, sc
     forward pass's.  `out` may pass the five tensors to reuse them (dh may be
     dh_out), `workspace` float32 scratch of at least
     fp8g_norm_residual_backward_workspace_bytes(rows, H) bytes."""
-    _rows(y, "y")
+    dev = _rows(y, "y")
     rows, H = y.shape
-    _shaped(h_out, y.dtype, (rows, H), "h_out")
+    _operand(h_out, y.dtype, (rows, H), dev, "h_out")
     for name, t in (("dz", dz), ("dh_out", dh_out)):
         if t is not None:
-            _shaped(t, y.dtype, (rows, H), name)
+            _operand(t, y.dtype, (rows, H), dev, name)
     kind = _norm_params(y, post_weight, gate, pre_weight)
-    dev = y.device
-    _all_on(dev, "h_out dz dh_out post_weight gate pre_weight", h_out, dz, dh_out, post_weight, gate, pre_weight)
     with _On(dev, stream) as raw:
         if out is None:
             out = (torch.empty_like(y), torch.empty_like(y), *(None if p is None else torch.empty_like(p)
                                                                 for p in (pre_weight, post_weight, gate)))
         dh, dy, dpre, dpost, dgate = out
-        _shaped(dh, y.dtype, (rows, H), "dh"), _shaped(dy, y.dtype, (rows, H), "dy")
+        _operand(dh, y.dtype, (rows, H), dev, "dh"), _operand(dy, y.dtype, (rows, H), dev, "dy")
         for name, p, d in (("dpre_weight", pre_weight, dpre), ("dpost_weight", post_weight, dpost),
                            ("dgate", gate, dgate)):
             if (p is None) != (d is None):
                 raise ValueError(f"{name}: an output exactly if its parameter is given")
             if d is not None:
-                _shaped(d, torch.float32, p.shape, name)
+                _operand(d, torch.float32, p.shape, dev, name)
         need = lib.fp8g_norm_residual_backward_workspace_bytes(rows, H)
         if workspace is None and need:
             workspace = torch.empty(need // 4, dtype=torch.float32, device=dev)
         elif workspace is not None:
-            _dev(workspace, torch.float32, "workspace")
-        _all_on(dev, "dh dy dpre_weight dpost_weight dgate workspace", dh, dy, dpre, dpost, dgate, workspace)
+            _operand(_dev(workspace, torch.float32, "workspace"), torch.float32, workspace.shape, dev, "workspace")
         _check(lib.fp8g_norm_residual_backward(_addr(dz), _addr(dh_out), h_out.data_ptr(), y.data_ptr(),
                                                _IN_DTYPE[y.dtype], rows, H, _addr(post_weight), _addr(gate), kind,
                                                scale, _addr(pre_weight), eps, dh.data_ptr(), dy.data_ptr(), _addr(dpre),
