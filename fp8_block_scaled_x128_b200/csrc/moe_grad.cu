@@ -38,7 +38,8 @@ constexpr int kPadBlocks = 256;  // most blocks of a padding CTA: its bitmap is 
 // alone zeroes 370 KB (45 rows of 4096 bf16) in some 15 us
 constexpr int kPadSlices = 8;
 // Routed slots up to which the sort may be one launch, while its CTAs are few
-// enough to run at once (SORTDIRECT).
+// enough to run at once (999 slots of 2112 FP32: 7.4 us against 8.0 with the
+// layout kernel, and one launch on the host).
 constexpr int kDirectSlots = 4096;
 
 // pos[r] if it names a row of the layout, -1 if the slot is dropped; anything

@@ -419,10 +419,12 @@ def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
             out = (torch.empty((G, Mmax, K), dtype=torch.uint8, device=dev),
                    torch.empty((G, K // 128, ld), dtype=torch.float32, device=dev),
                    torch.empty(R, dtype=torch.int32, device=dev), torch.empty(G, dtype=torch.int32, device=dev))
-        A, sa, pos, masked_m = out
-        _operand(A, torch.uint8, (G, Mmax, K), dev, "A")
-        _operand(sa, torch.float32, (G, K // 128, sa.shape[-1]), dev, "sa")
-        _operand(pos, torch.int32, (R,), dev, "pos"), _operand(masked_m, torch.int32, (G,), dev, "masked_m")
+            A, sa, pos, masked_m = out
+        else:
+            A, sa, pos, masked_m = out
+            _operand(A, torch.uint8, (G, Mmax, K), dev, "A")
+            _operand(sa, torch.float32, (G, K // 128, sa.shape[-1]), dev, "sa")
+            _operand(pos, torch.int32, (R,), dev, "pos"), _operand(masked_m, torch.int32, (G,), dev, "masked_m")
         _check(lib.fp8g_moe_dispatch_masked(x.data_ptr(), _IN_DTYPE[x.dtype], T, K, expert.data_ptr(), topk, G, Mmax,
                                             A.data_ptr(), sa.data_ptr(), sa.shape[-1], pos.data_ptr(),
                                             masked_m.data_ptr(), raw), "fp8g_moe_dispatch_masked")
@@ -463,8 +465,10 @@ def moe_permute_backward(dxs, pos, T, topk, out=None, stream=None):
     _layout_rows(M, "dxs")
     _operand(pos, torch.int32, (T * topk,), dev, "pos")
     with _On(dev, stream) as raw:
-        dx = torch.empty((T, N), dtype=dxs.dtype, device=dev) if out is None else out
-        _operand(dx, dxs.dtype, (T, N), dev, "out")
+        if out is None:
+            dx = torch.empty_strided((T, N), (N, 1), dtype=dxs.dtype, device=dev)
+        else:
+            dx = _operand(out, dxs.dtype, (T, N), dev, "out")
         _check(lib.fp8g_moe_permute_backward(dxs.data_ptr(), _IN_DTYPE[dxs.dtype], M // 128, N, pos.data_ptr(), T,
                                              topk, dx.data_ptr(), raw), "fp8g_moe_permute_backward")
     return dx
@@ -549,25 +553,28 @@ def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=
         _operand(h, y.dtype, (rows, H), dev, "h")
     kind = _norm_params(y, post_weight, gate, pre_weight)
     with _On(dev, stream) as raw:
-        if out is None:
-            if quantize:
-                out = (torch.empty_like(y), torch.empty((rows, H), dtype=torch.uint8, device=dev),
-                       torch.zeros((max(1, H // 128), max(4, (rows + 3) // 4 * 4)), dtype=torch.float32, device=dev))
-            else:
-                out = (torch.empty_like(y), torch.empty_like(y))
         z = q = sa = None
-        if quantize:
-            h_out, q, sa = out
-            _operand(q, torch.uint8, (rows, H), dev, "q"), _operand(sa, torch.float32, (H // 128, sa.shape[-1]), dev, "sa")
+        if out is None:
+            h_out = torch.empty_like(y)
+            if quantize:
+                q = torch.empty_like(y, dtype=torch.uint8)
+                sa = torch.zeros((max(1, H // 128), max(4, (rows + 3) // 4 * 4)), dtype=torch.float32, device=dev)
+            else:
+                z = torch.empty_like(y)
         else:
-            h_out, z = out
-            _operand(z, y.dtype, (rows, H), dev, "z")
-        _operand(h_out, y.dtype, (rows, H), dev, "h_out")
+            if quantize:
+                h_out, q, sa = out
+                _operand(q, torch.uint8, (rows, H), dev, "q")
+                _operand(sa, torch.float32, (H // 128, sa.shape[-1]), dev, "sa")
+            else:
+                h_out, z = out
+                _operand(z, y.dtype, (rows, H), dev, "z")
+            _operand(h_out, y.dtype, (rows, H), dev, "h_out")
         _check(lib.fp8g_norm_residual(y.data_ptr(), _addr(h), _IN_DTYPE[y.dtype], rows, H, _addr(post_weight),
                                       _addr(gate), kind, scale, _addr(pre_weight), eps, h_out.data_ptr(), _addr(z),
                                       _addr(q), _addr(sa), 0 if sa is None else sa.shape[-1], raw),
                "fp8g_norm_residual")
-    return out
+    return (h_out, q, sa) if quantize else (h_out, z)
 
 
 def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, scale=1.0, pre_weight=None, eps=1e-6,
@@ -587,28 +594,31 @@ def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, sc
     kind = _norm_params(y, post_weight, gate, pre_weight)
     with _On(dev, stream) as raw:
         if out is None:
-            out = (torch.empty_like(y), torch.empty_like(y), *(None if p is None else torch.empty_like(p)
-                                                                for p in (pre_weight, post_weight, gate)))
-        dh, dy, dpre, dpost, dgate = out
-        _operand(dh, y.dtype, (rows, H), dev, "dh"), _operand(dy, y.dtype, (rows, H), dev, "dy")
-        for name, p, d in (("dpre_weight", pre_weight, dpre), ("dpost_weight", post_weight, dpost),
-                           ("dgate", gate, dgate)):
-            if (p is None) != (d is None):
-                raise ValueError(f"{name}: an output exactly if its parameter is given")
-            if d is not None:
-                _operand(d, torch.float32, p.shape, dev, name)
-        need = lib.fp8g_norm_residual_backward_workspace_bytes(rows, H)
-        if workspace is None and need:
-            workspace = torch.empty(need // 4, dtype=torch.float32, device=dev)
-        elif workspace is not None:
-            _operand(_dev(workspace, torch.float32, "workspace"), torch.float32, workspace.shape, dev, "workspace")
+            dh, dy = torch.empty_like(y), torch.empty_like(y)
+            dpre = None if pre_weight is None else torch.empty_like(pre_weight)
+            dpost = None if post_weight is None else torch.empty_like(post_weight)
+            dgate = None if gate is None else torch.empty_like(gate)
+        else:
+            dh, dy, dpre, dpost, dgate = out
+            _operand(dh, y.dtype, (rows, H), dev, "dh"), _operand(dy, y.dtype, (rows, H), dev, "dy")
+            for name, p, d in (("dpre_weight", pre_weight, dpre), ("dpost_weight", post_weight, dpost),
+                               ("dgate", gate, dgate)):
+                if (p is None) != (d is None):
+                    raise ValueError(f"{name}: an output exactly if its parameter is given")
+                if d is not None:
+                    _operand(d, torch.float32, p.shape, dev, name)
+        if workspace is not None:
+            _operand(workspace, torch.float32, workspace.shape, dev, "workspace")
+        elif kind == 1 or pre_weight is not None or post_weight is not None:
+            need = lib.fp8g_norm_residual_backward_workspace_bytes(rows, H) // 4
+            workspace = torch.empty_strided((need,), (1,), dtype=torch.float32, device=dev)
         _check(lib.fp8g_norm_residual_backward(_addr(dz), _addr(dh_out), h_out.data_ptr(), y.data_ptr(),
                                                _IN_DTYPE[y.dtype], rows, H, _addr(post_weight), _addr(gate), kind,
                                                scale, _addr(pre_weight), eps, dh.data_ptr(), dy.data_ptr(), _addr(dpre),
                                                _addr(dpost), _addr(dgate), _addr(workspace),
                                                0 if workspace is None else workspace.numel() * 4, raw),
                "fp8g_norm_residual_backward")
-    return out
+    return dh, dy, dpre, dpost, dgate
 
 
 def bf16_gemm_nt(A, B, D=None, stream=None):

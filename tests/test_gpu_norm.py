@@ -227,6 +227,46 @@ def test_in_place_streams_and_graphs(g):
     assert torch.equal(over, second[0])
 
 
+@pytest.mark.parametrize("H", [256, 7168, 12000])
+def test_calls_at_once_on_two_streams_and_in_two_graphs(g, H):
+    """Two backward passes under way together, each with the workspace it makes
+    itself, and two captured ones replayed together, give what each gives alone."""
+    rows = 700
+    sides = []
+    for seed in (1, 2):
+        x, gen = inputs(seed, rows, H, torch.bfloat16, True, "channel", True, True)
+        dz, dho = (torch.randn(rows, H, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+        y, h = dev(x["y"]), dev(x["h"])
+        kw = dict(post_weight=dev(x["post_w"]), gate=dev(x["gate"]), scale=0.5, pre_weight=dev(x["pre_w"]), eps=EPS)
+        sides.append((dz, dho, y, h, kw))
+
+    def both(side, stream=None):
+        dz, dho, y, h, kw = side
+        h_out, z = g.norm_residual(y, h, stream=stream, **kw)
+        return (h_out, z, *g.norm_residual_backward(dz, dho, h_out, y, stream=stream, **kw))
+
+    want = [both(s) for s in sides]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    for _ in range(5):
+        got = [both(s, st) for s, st in zip(sides, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, q in zip(want, got) for a, b in zip(w, q))
+    graphs, outs = [], []
+    for s in sides:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(both(s))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, q in zip(want, outs) for a, b in zip(w, q))
+    assert g.device_error() == 0
+
+
 def test_the_same_call_gives_the_same_bits(g):
     x, gen = inputs(12, 1500, 1024, torch.bfloat16, True, "channel", True, True)
     dz = torch.randn(1500, 1024, generator=gen).to(torch.bfloat16).cuda()
