@@ -345,56 +345,42 @@ def moe_combine(D, pos, w, T, topk, out=None, stream=None):
     return out
 
 
-def _operand(t, dt, shape, dev, name):
-    """t, if it is a contiguous tensor of this type and shape (a tuple) on dev.
-    One check per operand, kept short: these calls are made per layer and
-    decoded token."""
-    if t.dtype != dt or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def _operand(t, dt, shape, index, name):
+    """t, if it is a contiguous CUDA tensor of this type and shape (a tuple) on
+    device `index`.  One short check per operand: these calls are made per layer
+    and decoded token."""
+    if t.dtype != dt or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        if t.is_cuda and t.get_device() != index:
+            raise ValueError(f"all operands must be on one device: {name} is on {t.device}, expected cuda:{index}")
         raise TypeError(f"{name}: expected a contiguous CUDA tensor of {dt} {tuple(shape)}, got {t.dtype} "
                         f"{tuple(t.shape)} on {t.device}")
-    if t.device != dev:
-        raise ValueError(f"all operands must be on one device: {name} is on {t.device}, expected {dev}")
     return t
 
 
 def _rows(t, name):
-    """The device of t, if it is a contiguous 2-D CUDA tensor of activations."""
+    """The device index of t, if it is a contiguous 2-D CUDA tensor of activations."""
     if t.dtype not in _IN_DTYPE or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous 2-D CUDA tensor of bfloat16 or float32, got {t.dtype} "
                         f"{tuple(t.shape)} on {t.device}")
-    return t.device
+    return t.get_device()
 
 
-# the raw handle of a device's current stream; without the Stream object of
-# torch.cuda.current_stream where torch has the short way
+# the current device and the raw handle of its current stream, without torch.cuda's
+# Stream object and initialisation check where torch has the short way
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _On:
-    """Runs a call under its operands' device and, if a stream is given, under
-    that stream, so that what the call allocates belongs to the stream it runs
-    on.  Entering gives the raw stream."""
-    __slots__ = ("dev", "stream", "ctx")
-
-    def __init__(self, dev, stream):
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the operands on {dev}")
-        self.dev, self.stream, self.ctx = dev, stream, None
-
-    def __enter__(self):
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-        elif self.dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.dev)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return _current_raw(self.dev.index) if self.stream is None else self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
+def _elsewhere(index, stream):
+    """What to enter before a call whose operands are on device `index`, or None
+    if that is the current device and no stream is given.  Under a given stream,
+    what the call allocates belongs to the stream it runs on."""
+    if stream is None:
+        return None if index == _current_device() else torch.cuda.device(index)
+    if stream.device != torch.device("cuda", index):
+        raise ValueError(f"stream is on {stream.device}, the operands on cuda:{index}")
+    return torch.cuda.stream(stream)
 
 
 def _addr(t):
@@ -413,21 +399,25 @@ def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
     topk, G, Mmax = int(topk), int(G), int(Mmax)
     R = T * topk
     _operand(expert, torch.int32, (R,), dev, "expert")
-    with _On(dev, stream) as raw:
-        if out is None:
-            ld = (Mmax + 3) // 4 * 4
-            out = (torch.empty((G, Mmax, K), dtype=torch.uint8, device=dev),
-                   torch.empty((G, K // 128, ld), dtype=torch.float32, device=dev),
-                   torch.empty(R, dtype=torch.int32, device=dev), torch.empty(G, dtype=torch.int32, device=dev))
-            A, sa, pos, masked_m = out
-        else:
-            A, sa, pos, masked_m = out
-            _operand(A, torch.uint8, (G, Mmax, K), dev, "A")
-            _operand(sa, torch.float32, (G, K // 128, sa.shape[-1]), dev, "sa")
-            _operand(pos, torch.int32, (R,), dev, "pos"), _operand(masked_m, torch.int32, (G,), dev, "masked_m")
-        _check(lib.fp8g_moe_dispatch_masked(x.data_ptr(), _IN_DTYPE[x.dtype], T, K, expert.data_ptr(), topk, G, Mmax,
-                                            A.data_ptr(), sa.data_ptr(), sa.shape[-1], pos.data_ptr(),
-                                            masked_m.data_ptr(), raw), "fp8g_moe_dispatch_masked")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_dispatch_masked(x, expert, topk, G, Mmax, out)
+    raw = _current_raw(dev)
+    if out is None:
+        ld = (Mmax + 3) // 4 * 4
+        out = (torch.empty((G, Mmax, K), dtype=torch.uint8, device=x.device),
+               torch.empty((G, K // 128, ld), dtype=torch.float32, device=x.device),
+               torch.empty(R, dtype=torch.int32, device=x.device), torch.empty(G, dtype=torch.int32, device=x.device))
+        A, sa, pos, masked_m = out
+    else:
+        A, sa, pos, masked_m = out
+        _operand(A, torch.uint8, (G, Mmax, K), dev, "A")
+        _operand(sa, torch.float32, (G, K // 128, sa.shape[-1]), dev, "sa")
+        _operand(pos, torch.int32, (R,), dev, "pos"), _operand(masked_m, torch.int32, (G,), dev, "masked_m")
+    _check(lib.fp8g_moe_dispatch_masked(x.data_ptr(), _IN_DTYPE[x.dtype], T, K, expert.data_ptr(), topk, G, Mmax,
+                                        A.data_ptr(), sa.data_ptr(), sa.shape[-1], pos.data_ptr(),
+                                        masked_m.data_ptr(), raw), "fp8g_moe_dispatch_masked")
     return A, sa, pos, masked_m
 
 
@@ -443,15 +433,19 @@ def moe_permute(x, expert, topk, G, blocks=None, out=None, stream=None):
     R = T * topk
     _operand(expert, torch.int32, (R,), dev, "expert")
     nb = moe_blocks(T, topk, G) if blocks is None else int(blocks)
-    with _On(dev, stream) as raw:
-        if out is None:
-            out = (torch.empty((nb * 128, N), dtype=x.dtype, device=dev),
-                   torch.empty(R, dtype=torch.int32, device=dev), torch.empty(nb, dtype=torch.int32, device=dev))
-        xs, pos, mi = out
-        _operand(xs, x.dtype, (nb * 128, N), dev, "xs")
-        _operand(pos, torch.int32, (R,), dev, "pos"), _operand(mi, torch.int32, (nb,), dev, "m_indices")
-        _check(lib.fp8g_moe_permute(x.data_ptr(), _IN_DTYPE[x.dtype], T, N, expert.data_ptr(), topk, G, nb,
-                                    xs.data_ptr(), pos.data_ptr(), mi.data_ptr(), raw), "fp8g_moe_permute")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_permute(x, expert, topk, G, blocks, out)
+    raw = _current_raw(dev)
+    if out is None:
+        out = (torch.empty((nb * 128, N), dtype=x.dtype, device=x.device),
+               torch.empty(R, dtype=torch.int32, device=x.device), torch.empty(nb, dtype=torch.int32, device=x.device))
+    xs, pos, mi = out
+    _operand(xs, x.dtype, (nb * 128, N), dev, "xs")
+    _operand(pos, torch.int32, (R,), dev, "pos"), _operand(mi, torch.int32, (nb,), dev, "m_indices")
+    _check(lib.fp8g_moe_permute(x.data_ptr(), _IN_DTYPE[x.dtype], T, N, expert.data_ptr(), topk, G, nb,
+                                xs.data_ptr(), pos.data_ptr(), mi.data_ptr(), raw), "fp8g_moe_permute")
     return xs, pos, mi
 
 
@@ -464,13 +458,17 @@ def moe_permute_backward(dxs, pos, T, topk, out=None, stream=None):
     T, topk = int(T), int(topk)
     _layout_rows(M, "dxs")
     _operand(pos, torch.int32, (T * topk,), dev, "pos")
-    with _On(dev, stream) as raw:
-        if out is None:
-            dx = torch.empty_strided((T, N), (N, 1), dtype=dxs.dtype, device=dev)
-        else:
-            dx = _operand(out, dxs.dtype, (T, N), dev, "out")
-        _check(lib.fp8g_moe_permute_backward(dxs.data_ptr(), _IN_DTYPE[dxs.dtype], M // 128, N, pos.data_ptr(), T,
-                                             topk, dx.data_ptr(), raw), "fp8g_moe_permute_backward")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_permute_backward(dxs, pos, T, topk, out)
+    raw = _current_raw(dev)
+    if out is None:
+        dx = torch.empty_strided((T, N), (N, 1), dtype=dxs.dtype, device=dxs.device)
+    else:
+        dx = _operand(out, dxs.dtype, (T, N), dev, "out")
+    _check(lib.fp8g_moe_permute_backward(dxs.data_ptr(), _IN_DTYPE[dxs.dtype], M // 128, N, pos.data_ptr(), T,
+                                         topk, dx.data_ptr(), raw), "fp8g_moe_permute_backward")
     return dx
 
 
@@ -491,39 +489,43 @@ def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, str
     _dev(D, torch.bfloat16, "D")
     M, N = D.shape
     _layout_rows(M, "D")
-    dev = D.device
+    dev = D.get_device()
     _operand(dout, torch.bfloat16, (T, N), dev, "dout"), _operand(pos, torch.int32, (T * topk,), dev, "pos")
     if w is not None:
         _operand(w, torch.float32, (T * topk,), dev, "w")
-    with _On(dev, stream) as raw:
-        if out is None:
-            dw = None if w is None else torch.empty(T * topk, dtype=torch.float32, device=dev)
-            if quantize:
-                out = (torch.empty((M, N), dtype=torch.uint8, device=dev),
-                       torch.empty((N // 128, max(M, 4)), dtype=torch.float32, device=dev), dw)
-            else:
-                out = (torch.empty((M, N), dtype=torch.bfloat16, device=dev), dw)
-        q = sa = dD = None
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_combine_backward(dout, D, pos, w, T, topk, quantize, out)
+    raw = _current_raw(dev)
+    if out is None:
+        dw = None if w is None else torch.empty(T * topk, dtype=torch.float32, device=D.device)
         if quantize:
-            q, sa, dw = out
-            _operand(q, torch.uint8, (M, N), dev, "q"), _operand(sa, torch.float32, (N // 128, sa.shape[-1]), dev, "sa")
+            out = (torch.empty((M, N), dtype=torch.uint8, device=D.device),
+                   torch.empty((N // 128, max(M, 4)), dtype=torch.float32, device=D.device), dw)
         else:
-            dD, dw = out
-            _operand(dD, torch.bfloat16, (M, N), dev, "dD")
-        if (dw is None) != (w is None):
-            raise ValueError("dw: an output exactly if w is given")
-        if dw is not None:
-            _operand(dw, torch.float32, (T * topk,), dev, "dw")
-        _check(lib.fp8g_moe_combine_backward(dout.data_ptr(), D.data_ptr(), N, pos.data_ptr(), _addr(w), T, topk,
-                                             M // 128, _addr(dD), _addr(q), _addr(sa),
-                                             0 if sa is None else sa.shape[-1], _addr(dw), raw),
-               "fp8g_moe_combine_backward")
+            out = (torch.empty((M, N), dtype=torch.bfloat16, device=D.device), dw)
+    q = sa = dD = None
+    if quantize:
+        q, sa, dw = out
+        _operand(q, torch.uint8, (M, N), dev, "q"), _operand(sa, torch.float32, (N // 128, sa.shape[-1]), dev, "sa")
+    else:
+        dD, dw = out
+        _operand(dD, torch.bfloat16, (M, N), dev, "dD")
+    if (dw is None) != (w is None):
+        raise ValueError("dw: an output exactly if w is given")
+    if dw is not None:
+        _operand(dw, torch.float32, (T * topk,), dev, "dw")
+    _check(lib.fp8g_moe_combine_backward(dout.data_ptr(), D.data_ptr(), N, pos.data_ptr(), _addr(w), T, topk,
+                                         M // 128, _addr(dD), _addr(q), _addr(sa),
+                                         0 if sa is None else sa.shape[-1], _addr(dw), raw),
+           "fp8g_moe_combine_backward")
     return out
 
 
 def _norm_params(y, post_weight, gate, pre_weight):
     """Checks the parameters of rows y; the kind of the gate."""
-    (rows, H), dev = y.shape, y.device
+    (rows, H), dev = y.shape, y.get_device()
     if post_weight is not None:
         _operand(post_weight, torch.float32, (H,), dev, "post_weight")
     if pre_weight is not None:
@@ -552,28 +554,32 @@ def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=
     if h is not None:
         _operand(h, y.dtype, (rows, H), dev, "h")
     kind = _norm_params(y, post_weight, gate, pre_weight)
-    with _On(dev, stream) as raw:
-        z = q = sa = None
-        if out is None:
-            h_out = torch.empty_like(y)
-            if quantize:
-                q = torch.empty_like(y, dtype=torch.uint8)
-                sa = torch.zeros((max(1, H // 128), max(4, (rows + 3) // 4 * 4)), dtype=torch.float32, device=dev)
-            else:
-                z = torch.empty_like(y)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return norm_residual(y, h, post_weight, gate, scale, pre_weight, eps, quantize, out)
+    raw = _current_raw(dev)
+    z = q = sa = None
+    if out is None:
+        h_out = torch.empty_like(y)
+        if quantize:
+            q = torch.empty_like(y, dtype=torch.uint8)
+            sa = torch.zeros((max(1, H // 128), max(4, (rows + 3) // 4 * 4)), dtype=torch.float32, device=y.device)
         else:
-            if quantize:
-                h_out, q, sa = out
-                _operand(q, torch.uint8, (rows, H), dev, "q")
-                _operand(sa, torch.float32, (H // 128, sa.shape[-1]), dev, "sa")
-            else:
-                h_out, z = out
-                _operand(z, y.dtype, (rows, H), dev, "z")
-            _operand(h_out, y.dtype, (rows, H), dev, "h_out")
-        _check(lib.fp8g_norm_residual(y.data_ptr(), _addr(h), _IN_DTYPE[y.dtype], rows, H, _addr(post_weight),
-                                      _addr(gate), kind, scale, _addr(pre_weight), eps, h_out.data_ptr(), _addr(z),
-                                      _addr(q), _addr(sa), 0 if sa is None else sa.shape[-1], raw),
-               "fp8g_norm_residual")
+            z = torch.empty_like(y)
+    else:
+        if quantize:
+            h_out, q, sa = out
+            _operand(q, torch.uint8, (rows, H), dev, "q")
+            _operand(sa, torch.float32, (H // 128, sa.shape[-1]), dev, "sa")
+        else:
+            h_out, z = out
+            _operand(z, y.dtype, (rows, H), dev, "z")
+        _operand(h_out, y.dtype, (rows, H), dev, "h_out")
+    _check(lib.fp8g_norm_residual(y.data_ptr(), _addr(h), _IN_DTYPE[y.dtype], rows, H, _addr(post_weight),
+                                  _addr(gate), kind, scale, _addr(pre_weight), eps, h_out.data_ptr(), _addr(z),
+                                  _addr(q), _addr(sa), 0 if sa is None else sa.shape[-1], raw),
+           "fp8g_norm_residual")
     return (h_out, q, sa) if quantize else (h_out, z)
 
 
@@ -592,32 +598,36 @@ def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, sc
         if t is not None:
             _operand(t, y.dtype, (rows, H), dev, name)
     kind = _norm_params(y, post_weight, gate, pre_weight)
-    with _On(dev, stream) as raw:
-        if out is None:
-            dh, dy = torch.empty_like(y), torch.empty_like(y)
-            dpre = None if pre_weight is None else torch.empty_like(pre_weight)
-            dpost = None if post_weight is None else torch.empty_like(post_weight)
-            dgate = None if gate is None else torch.empty_like(gate)
-        else:
-            dh, dy, dpre, dpost, dgate = out
-            _operand(dh, y.dtype, (rows, H), dev, "dh"), _operand(dy, y.dtype, (rows, H), dev, "dy")
-            for name, p, d in (("dpre_weight", pre_weight, dpre), ("dpost_weight", post_weight, dpost),
-                               ("dgate", gate, dgate)):
-                if (p is None) != (d is None):
-                    raise ValueError(f"{name}: an output exactly if its parameter is given")
-                if d is not None:
-                    _operand(d, torch.float32, p.shape, dev, name)
-        if workspace is not None:
-            _operand(workspace, torch.float32, workspace.shape, dev, "workspace")
-        elif kind == 1 or pre_weight is not None or post_weight is not None:
-            need = lib.fp8g_norm_residual_backward_workspace_bytes(rows, H) // 4
-            workspace = torch.empty_strided((need,), (1,), dtype=torch.float32, device=dev)
-        _check(lib.fp8g_norm_residual_backward(_addr(dz), _addr(dh_out), h_out.data_ptr(), y.data_ptr(),
-                                               _IN_DTYPE[y.dtype], rows, H, _addr(post_weight), _addr(gate), kind,
-                                               scale, _addr(pre_weight), eps, dh.data_ptr(), dy.data_ptr(), _addr(dpre),
-                                               _addr(dpost), _addr(dgate), _addr(workspace),
-                                               0 if workspace is None else workspace.numel() * 4, raw),
-               "fp8g_norm_residual_backward")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return norm_residual_backward(dz, dh_out, h_out, y, post_weight, gate, scale, pre_weight, eps, out, workspace)
+    raw = _current_raw(dev)
+    if out is None:
+        dh, dy = torch.empty_like(y), torch.empty_like(y)
+        dpre = None if pre_weight is None else torch.empty_like(pre_weight)
+        dpost = None if post_weight is None else torch.empty_like(post_weight)
+        dgate = None if gate is None else torch.empty_like(gate)
+    else:
+        dh, dy, dpre, dpost, dgate = out
+        _operand(dh, y.dtype, (rows, H), dev, "dh"), _operand(dy, y.dtype, (rows, H), dev, "dy")
+        for name, p, d in (("dpre_weight", pre_weight, dpre), ("dpost_weight", post_weight, dpost),
+                           ("dgate", gate, dgate)):
+            if (p is None) != (d is None):
+                raise ValueError(f"{name}: an output exactly if its parameter is given")
+            if d is not None:
+                _operand(d, torch.float32, p.shape, dev, name)
+    if workspace is not None:
+        _operand(workspace, torch.float32, workspace.shape, dev, "workspace")
+    elif kind == 1 or pre_weight is not None or post_weight is not None:
+        need = lib.fp8g_norm_residual_backward_workspace_bytes(rows, H) // 4
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.float32, device=y.device)
+    _check(lib.fp8g_norm_residual_backward(_addr(dz), _addr(dh_out), h_out.data_ptr(), y.data_ptr(),
+                                           _IN_DTYPE[y.dtype], rows, H, _addr(post_weight), _addr(gate), kind,
+                                           scale, _addr(pre_weight), eps, dh.data_ptr(), dy.data_ptr(), _addr(dpre),
+                                           _addr(dpost), _addr(dgate), _addr(workspace),
+                                           0 if workspace is None else workspace.numel() * 4, raw),
+           "fp8g_norm_residual_backward")
     return dh, dy, dpre, dpost, dgate
 
 

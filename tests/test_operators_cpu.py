@@ -143,6 +143,7 @@ def test_good_arguments_reach_the_device(gemm, name, good):
 def fake(shape, dtype=torch.bfloat16, index=0):
     t = FakeCudaTensor(shape, dtype, index)
     t.dim = lambda: len(shape)
+    t.get_device = lambda: index
     return t
 
 
