@@ -303,30 +303,25 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
       s_w[k] = k < topk && w ? __ldg(w + t * topk + k) : 1.f;
     }
     __syncthreads();
-    // this thread's columns of the next vectors to fetch, and of the current ones
-    const uint16_t* dout_at = dout + t * N + 8 * threadIdx.x;
-    const uint16_t* D_at = D + 8 * threadIdx.x;
-    long col = 8 * threadIdx.x;
-    int fetch_j = threadIdx.x;
+    const uint16_t* dout_t = dout + t * N;
+    long col = 8 * threadIdx.x;   // this thread's columns: of the current vectors,
+    int fetch_col = static_cast<int>(col);  // and of the next ones to fetch
     uint32_t put = slot0, get = slot0;
-    // copies the vectors of slots gi * kGroup ..; zeros for columns behind the
-    // row's end, whose products then add nothing
+    // Copies the vectors of slots gi * kGroup ..; zeros for dropped slots and for
+    // columns behind the row's end, whose products then add nothing.
     auto fetch = [&](int gi, bool there) {
       if (there) {
-        const bool in = fetch_j < per_row;
-        if (gi == 0) {
-          if (in) cp_async16(put, dout_at);
-          else fp8g::st_shared_v4(put, make_uint4(0u, 0u, 0u, 0u));
-        }
+        const bool in = fetch_col < N;
+        const int c = in ? fetch_col : 0;
+        if (gi == 0) cp_async16_or_zero(put, dout_t + c, in ? 16 : 0);
         if (dw) {
 #pragma unroll
           for (int k = 0; k < kGroup; ++k) {
             const long row = s_row[gi * kGroup + k];
-            if (!in) fp8g::st_shared_v4(put + (k + 1) * pitch, make_uint4(0u, 0u, 0u, 0u));
-            else if (row >= 0) cp_async16(put + (k + 1) * pitch, D_at + row);
+            cp_async16_or_zero(put + (k + 1) * pitch, D + (row < 0 ? 0 : row) + c, in && row >= 0 ? 16 : 0);
           }
         }
-        if (gi == kGroups - 1) dout_at += 8 * step, D_at += 8 * step, fetch_j += step;
+        if (gi == kGroups - 1) fetch_col += 8 * step;
       }
       cp_commit();
       put = put == slot0 ? slot0 + stage : slot0;
@@ -356,7 +351,7 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
             for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             amax *= fabsf(s_w[own]);
             tiny = __any_sync(0xffffffffu, amax > 0.f && amax < fp8g::quant::kTinyAmax);
-            own_s = tiny ? fp8g::quant::scale_of(amax) : fp8g::quant::normal_scale(amax);
+            own_s = tiny ? fp8g::quant::any_scale(amax) : fp8g::quant::normal_scale(amax);
             own_y = __frcp_rn(own_s);
             if (in && (lane & 15) < kSlots && s_pos[own] >= 0) sa[(col >> 7) * ld_sa + s_pos[own]] = own_s;
           }
@@ -445,7 +440,7 @@ int row_threads(long vecs) {
 }
 
 int check_slots(int T, int topk, int N) {
-  if (T < 0 || topk < 1 || topk > kMaxTopk || N < 1 || static_cast<long>(T) * topk > 0x7FFFFFFFL)
+  if (T < 0 || topk < 1 || topk > kMaxTopk || N < 1 || N > 1 << 20 || static_cast<long>(T) * topk > 0x7FFFFFFFL)
     return FP8G_ERR_INVALID_ARG;
   return FP8G_OK;
 }
@@ -468,7 +463,6 @@ extern "C" int fp8g_moe_permute(const void* x, int x_dtype, int T, int N, const 
   uint32_t* err = fp8g::device_error_word();
   if (sms <= 0 || !err) return FP8G_ERR_CUDA;
   const long vecs = static_cast<long>(N) * (x_dtype == FP8G_IN_F32 ? 4 : 2) / 16;
-  if (vecs > 0x7FFFFFFFL) return FP8G_ERR_INVALID_ARG;
   const int parts = static_cast<int>((vecs + 255) / 256);
   if (R > 0 && R <= kDirectSlots && static_cast<long>(T) * parts <= 8L * sms) {
     const int pads = std::min(G * kPadSlices, 2 * sms);
@@ -549,6 +543,7 @@ extern "C" int fp8g_moe_combine_backward(const uint16_t* dout, const uint16_t* D
   const int sms = sm_count();
   uint32_t* err = fp8g::device_error_word();
   if (sms <= 0 || !err) return FP8G_ERR_CUDA;
+  if (blocks == 0) D = dout;  // no row is read, but copies of no bytes name one
   const int pads = pad_ctas(blocks, sms);
   const unsigned grid = static_cast<unsigned>(pads + std::min<long>(T, 32L * sms));
   const int threads = row_threads(N / 8);

@@ -44,7 +44,14 @@ __device__ __forceinline__ void normal_codes(const rows::Pair8& neg, float s, fl
   for (int i = 0; i < 2; ++i) c[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | (e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16);
 }
 
-// The general path, for groups of any magnitude.
+// The general path, for groups of any magnitude.  amax / 448 rounds to zero below
+// 3.2e-43; such a group, whose quotients the definition leaves without a value
+// (x / 0), is an all-zero group: scale 1, codes of zeros.
+__device__ __forceinline__ float any_scale(float amax) {
+  const float s = scale_of(amax);
+  return s > 0.f ? s : 1.f;
+}
+
 __device__ __forceinline__ void any_codes(const rows::Pair8& neg, float s, uint32_t (&c)[2]) {
   float v[8];
   rows::values_of(neg, v);
@@ -57,7 +64,7 @@ __device__ __forceinline__ void any_codes(const rows::Pair8& neg, float s, uint3
 // given the values' negatives.  All 32 lanes call it.
 __device__ __forceinline__ void quantize8(const rows::Pair8& neg, float amax, float& s, uint32_t (&c)[2]) {
   if (__any_sync(0xffffffffu, amax > 0.f && amax < kTinyAmax)) {
-    s = scale_of(amax);
+    s = any_scale(amax);
     any_codes(neg, s, c);
   } else {
     s = normal_scale(amax);

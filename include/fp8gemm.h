@@ -286,9 +286,11 @@ int fp8g_moe_combine(const uint16_t *D, int N, const int32_t *pos, const float *
  * fp8g_moe_dispatch, in front of m_grouped_fp8_gemm_nt_masked (GeekNews,
  * "마스킹(masked) 레이아웃의 그룹화 GEMM").  Expert g's slots, in their order r,
  * take rows 0, 1, ... of group g; token t is quantised per 1x128 group as by
- * fp8g_quantize_1x128.
+ * fp8g_quantize_1x128.  (Here and in the calls below a group so small that its
+ * scale would round to zero, amax < 3.2e-43, counts as an all-zero group.)
  *   x [T][K] (bf16 patterns or FP32, x_dtype), K % 128 == 0, K <= 65536;
- *   expert [T*topk] int32, -1 = dropped; 1 <= topk <= 16; 1 <= G <= 256;
+ *   x finite; expert [T*topk] int32, -1 = dropped; 1 <= topk <= 16;
+ *   1 <= G <= 256;
  *   outputs A [G][Mmax][K] e4m3 codes, sa [G][K/128][ld_sa] (ld_sa >= Mmax,
  *   ld_sa % 4 == 0), masked_m [G] rows of each group, and pos [T*topk], the
  *   slot's row g*Mmax + rank, or -1.  fp8g_moe_combine takes pos with the
@@ -309,7 +311,7 @@ int fp8g_moe_dispatch_masked(const void *x, int x_dtype, int T, int K,
 /*
  * Expert sort without quantisation: rows of x in the contiguous layout of
  * fp8g_moe_dispatch (same pos, m_indices, segments and capacity), in x's type.
- *   x [T][N] (bf16 patterns or FP32, x_dtype), N % 8 == 0, N >= 8;
+ *   x [T][N] (bf16 patterns or FP32, x_dtype), N % 8 == 0, 8 <= N <= 2^20;
  *   xs [blocks*128][N]: xs[pos[r]] = x[r / topk]; padding rows of every
  *   segment are zero, rows of unused blocks are not written.
  * topk, G, blocks, expert, pos, m_indices and their errors as in
@@ -326,7 +328,7 @@ int fp8g_moe_permute(const void *x, int x_dtype, int T, int N,
  * layout [blocks*128] that no other slot has.  An entry outside the layout
  * is skipped and sets FP8G_DEVERR_BAD_POS; a row named twice sets the same
  * flag (found by fp8g_moe_combine_backward, whose output it would leave
- * undefined).  1 <= topk <= 16, N % 8 == 0, N >= 8.
+ * undefined).  1 <= topk <= 16, N % 8 == 0, 8 <= N <= 2^20.
  *
  * fp8g_moe_permute_backward: dx[t] = sum over k of dxs[pos[t*topk + k]], FP32
  *   in slot order, rounded once; dropped slots add nothing.  It is the
@@ -338,7 +340,8 @@ int fp8g_moe_permute(const void *x, int x_dtype, int T, int N,
  *     dD[pos[r]] = w[r] * dout[t]       (one FP32 product)
  *     dw[r]      = sum over n of dout[t][n] * D[pos[r]][n]   (FP32; 0 if dropped)
  *   dout [T][N], D [blocks*128][N] bf16 patterns; w [T*topk] or NULL (weights
- *   of 1); dw [T*topk], or NULL to skip it (D is not read then).
+ *   of 1); dw [T*topk], or NULL to skip it (D is not read then).  Codes need
+ *   finite products.
  *   The rows leave in one of two forms, the other's pointer being NULL:
  *     dD [blocks*128][N] bf16 patterns, rounded once; or
  *     q [blocks*128][N] e4m3 codes and sa [N/128][ld_sa] scales of the FP32
@@ -372,7 +375,7 @@ int fp8g_moe_combine_backward(const uint16_t *dout, const uint16_t *D, int N,
  *   either z [rows][H] of type `dtype`, or q [rows][H] e4m3 codes with sa
  *   [H/128][ld_sa] scales (of the FP32 z, as fp8g_quantize_1x128 makes them;
  *   H % 128 == 0, ld_sa >= rows, ld_sa % 4 == 0; entries past `rows` are not
- *   written); the other's pointer is NULL.
+ *   written; z must be finite); the other's pointer is NULL.
  * 8 <= H <= 16384, H % 8 == 0; eps > 0; scale finite.  h_out may be h's
  * buffer and z may be y's; otherwise outputs overlap no input.
  * rows == 0 is a no-op.  One launch, no workspace.

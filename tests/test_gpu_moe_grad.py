@@ -143,6 +143,43 @@ def test_combine_backward_rows_and_weights(g, T, topk, G, N, drop):
     assert g.device_error() == 0
 
 
+def test_codes_of_tiny_and_huge_values(g):
+    """Groups far below and above 1, subnormal products and scales, zeros of both
+    signs: codes and scales of the definition, bit for bit."""
+    T, topk, N = 24, 3, 384
+    rng = np.random.default_rng(7)
+    x = tokens(8, T, N)
+    x[:, ::5] = 0
+    x[:, 1::5] = -0.0
+    x[3] = 0
+    w = np.array([1, -1, 0, 1e-30, 1e-38, 1e-42, 1.4e-45, 1e30, 3e36, -2.5, 1e-25, 8e-25], np.float32)[
+        rng.integers(0, 12, T * topk)]
+    pos = rng.permutation(256)[:T * topk].astype(np.int32)
+    prod = w[:, None] * synth.round_to_bf16(x)[np.arange(T * topk) // topk]
+    assert np.isfinite(prod).all()
+    eq, es = oracle.quantize_1x128(np.ascontiguousarray(prod))
+    # w = 1.4e-45 (2^-149): |prod| <= 2^-146, and 2^-146 / 448 < 2^-150 rounds to a
+    # scale of zero, where the definition divides by zero; such a group counts as
+    # all-zero: scale 1, zero codes with the values' signs
+    gone = es[:, :T * topk].T == 0
+    assert gone.any() and np.abs(prod).reshape(T * topk, -1, 128).max(-1)[gone].max() <= 2.0 ** -146
+    es[:, :T * topk][gone.T] = 1
+    eq = np.where(np.repeat(gone, 128, 1), np.signbit(prod) * np.uint8(0x80), eq)
+    D = torch.zeros(256, N, dtype=torch.bfloat16, device="cuda")
+    q, sa, _ = g.moe_combine_backward(cuda(x, torch.bfloat16), D, cuda(pos), cuda(w), T, topk, quantize=True)
+    assert np.array_equal(host(sa)[:, pos], es[:, :T * topk]) and np.array_equal(host(q)[pos], eq)
+    for scale in (1e-38, 1e-30, 1e-20, 1.0, 1e30):
+        xs = (x * np.float32(scale)).astype(np.float32)
+        e = rng.integers(0, 4, T * topk).astype(np.int32)
+        A, s, p, m = g.moe_dispatch_masked(cuda(xs), cuda(e), topk, 4, T * topk)
+        wp, wm, wq, ws, _ = masked_reference(xs, e, topk, 4, T * topk)
+        assert np.array_equal(host(p), wp)
+        tok = np.arange(T * topk) // topk
+        assert np.array_equal(host(A).reshape(-1, N)[wp], wq[tok])
+        assert np.array_equal(host(s)[wp // (T * topk), :, wp % (T * topk)], ws[:, tok].T)
+    assert g.device_error() == 0
+
+
 def test_bad_positions_are_flagged_and_skipped(g):
     T, topk, N = 6, 2, 128
     pos = np.array([0, 1, 128, 3, -9, 4, 127, 5, 1 << 30, 6, -1, 7], np.int32)   # 128, -9 and 2^30 are no rows

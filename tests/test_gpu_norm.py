@@ -104,6 +104,19 @@ def test_quantised_output_is_the_quantiser_of_z(g, rows, H, post, gate):
         assert torch.equal(h_out, call(g, xs)[0])
 
 
+@pytest.mark.parametrize("size", [1e-36, 1e-24, 1e-10, 1e12])
+def test_quantised_tiny_and_huge_rows(g, size):
+    """Pre-weights that bring z near either end of FP32: the fused codes are
+    still the quantiser's of the FP32 z."""
+    x, _ = inputs(17, 9, 640, torch.float32, True, "channel", True, True)
+    x["pre_w"] *= size
+    x["pre_w"][::7] = -0.0
+    _, z = call(g, x)
+    _, q, sa = call(g, x, quantize=True)
+    eq, esa = oracle.quantize_1x128(z.cpu().numpy(), ld_sa=sa.shape[1])
+    assert np.array_equal(sa.cpu().numpy()[:, :9], esa[:, :9]) and np.array_equal(q.cpu().numpy(), eq)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("rows,H,post,gate,res,pre", CASES)
 def test_backward_matches_the_formulas(g, rows, H, post, gate, res, pre, dtype):

@@ -48,6 +48,7 @@ PERMUTE = dict(x=P, dt=0, T=4, N=64, expert=P, topk=2, G=8, blocks=9, xs=P, pos=
 
 @pytest.mark.parametrize("status,changed", [
     (INVALID, dict(dt=-1)), (INVALID, dict(T=-1)), (INVALID, dict(N=0)), (MISALIGNED, dict(N=60)),
+    (INVALID, dict(N=(1 << 20) + 8)),
     (INVALID, dict(topk=0)), (INVALID, dict(topk=17)), (INVALID, dict(G=0)), (INVALID, dict(G=257)),
     (INVALID, dict(blocks=8)), (INVALID, dict(blocks=1 << 24)), (INVALID, dict(T=1 << 30, topk=4, blocks=1 << 23)),
     (INVALID, dict(x=None)), (INVALID, dict(expert=None)), (INVALID, dict(xs=None)), (INVALID, dict(pos=None)),
