@@ -105,7 +105,9 @@ __device__ __forceinline__ void pad_range(int cta, int pads, int blocks, int& b0
 // CTAs [0, pads) zero padding rows; the others take a part of a token's row
 // each, one 16-byte vector a thread, whatever the type: short CTAs leave little
 // work behind when the last ones run (with a CTA per token, 3.5 waves of 8 CTAs
-// an SM, the last wave ran half empty).
+// an SM, the last wave ran half empty).  4096 tokens x top-8 over 64 experts, 7168
+// bf16: 103 us with the layout kernel (of which some 7 us are not hidden), 588 MB
+// with the padding rows: 0.87 of the measured copy bandwidth.
 template <int kCap>
 __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int parts, int T, int topk,
                                                           const int32_t* __restrict__ pos, uint4* __restrict__ xs, int M,
@@ -220,6 +222,9 @@ __global__ void __launch_bounds__(256) moe_permute_direct_kernel(const uint4* __
   }
 }
 
+// A CTA per token: all of a thread's row loads are issued before the first
+// addition, which run in slot order.  The rows above, 529 MB: 77 us, 1.05 of the
+// measured copy bandwidth (reads outweigh writes, part of which stay in L2).
 template <bool kF32, int kCap>
 __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* __restrict__ dxs, int N,
                                                                    const int32_t* __restrict__ pos, int T, int topk,
@@ -253,8 +258,9 @@ __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* _
 // a thread), four slots at a time.  A thread copies its own vectors of the next
 // four slots' D rows (and of dout) into shared memory (cp.async) before it works
 // on the current ones, so loads are under way all the time without holding
-// registers.  FP32x2 instructions: with bf16 out the kernel is bound by HBM, with
-// codes out by instructions issued.
+// registers.  The same rows, 1.06 GB with the padding: 176 us to bf16, 0.92 of the
+// measured copy bandwidth; 0.80 GB to codes: 147 us, 0.83, with 60 % of the issue
+// slots used (packed FP32x2 arithmetic throughout).
 //
 // kQuant: the rows leave as e4m3 codes and 1x128 scales; 16 lanes hold a group
 // of columns.  Its largest |w x| is |w| times its largest |x|, rounded once

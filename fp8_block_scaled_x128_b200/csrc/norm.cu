@@ -171,6 +171,12 @@ __device__ __forceinline__ void keep8(uint32_t at, const Pair8& p) {
 
 __device__ __forceinline__ Pair8 kept8(uint32_t at) { return pairs_of<true>(load8_shared<true>(at)); }
 
+// The CTAs of a cluster end together: none is gone while another, whose waits may
+// have been given up, still sends to it.
+__device__ __forceinline__ void leave_together() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // Stages: two where two CTAs share an SM (bf16, two vectors a thread), else three.
 __host__ __device__ constexpr int forward_stages(bool f32, int vecs) { return !f32 && vecs == 2 ? 2 : 3; }
 // The backward pass: three for bf16 rows of one CTA, two where three do not fit.
@@ -186,6 +192,13 @@ constexpr int backward_regs(bool f32, int vecs) { return vecs == 2 ? 128 : f32 ?
 // Threads of an SM whose registers fit: each of its four parts has 16384.
 constexpr int threads_at(int regs) { return 128 * (16384 / (32 * regs)); }
 
+// Forward.  Each element of y and h is read once and each of h' and z written
+// once.  8192 x 7168 bf16 with post-norm and channel gate: 79.5 us, 5.9 TB/s, 0.90
+// of the measured copy bandwidth (32768 x 1024: 46 us, 0.89; 4096 x 16384: 104 us,
+// 0.79); two CTAs share an SM, so that one computes while the other waits for a
+// sum.  With codes out 89 us, 0.71: the quantisation adds a third to the
+// instructions, and the issue slots (57 %) and the sums' latency bound it.  One
+// row of 7168, decode's form: 4.1 us, two sums' latencies behind one load.
 template <bool kF32, int V, int kC, bool kQuant>
 __global__ void __launch_bounds__(kMaxThreads, 2)
     norm_residual_kernel(const void* y, const void* h, Shape S, Params P, void* h_out, void* z, uint8_t* q, float* sa,
@@ -279,6 +292,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     }
     at += src.step_bytes;
   }
+  if constexpr (kC > 1) leave_together();
 }
 
 // Backward.  Each cluster walks its rows and keeps, per column, the two sums
@@ -294,6 +308,12 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
 // dh_out + r1 dn - r1 <dn n> n), so a row takes one; the extra products and
 // reads of shared memory made a single CTA slower (8192 x 7168 bf16: 150 us
 // against 132).
+//
+// 8192 x 7168 bf16: 131 us with the parameter sums, 5.4 TB/s, 0.82 of the measured
+// copy bandwidth; 14 warps an SM at 128 registers, 48 % of the issue slots, the
+// rest waits for the two sums.  32768 x 1024: 84 us (0.73, instructions issued);
+// 4096 x 16384: 201 us (0.61) and 4096 x 7168 FP32 149 us (0.72), shared memory
+// and the clusters' sums.
 template <bool kF32, int V, int D, int kC>
 __global__ void __maxnreg__(backward_regs(kF32, V))
     norm_residual_backward_kernel(const void* dz, const void* dh_out, const void* h, const void* y, Shape S, Params P,
@@ -426,6 +446,7 @@ __global__ void __maxnreg__(backward_regs(kF32, V))
       reinterpret_cast<float4*>(pu)[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
   }
+  if constexpr (kC > 1) leave_together();
 }
 
 // Sums of partial rows part[2][P][H] over P.  A CTA takes 32 columns and the

@@ -181,7 +181,7 @@ __device__ __forceinline__ float warp_sums(const float (&v)[1]) { return warp_su
 // barriers, 149 without).  A CTA writes a
 // peer's buffer again only after it has the peer's sums of the call in between,
 // which every warp of the peer sends after reading the buffer; and it leaves
-// only after all sums sent to it have arrived.
+// after all sums sent to it have arrived.
 template <int n, int kC>
 struct RowSum {
   float s[2][n][16 * kC];
@@ -276,8 +276,6 @@ __device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src) {
   cp_async16(dst, src);
   if constexpr (kF32) cp_async16(dst + 16, src + 16);
 }
-
-__device__ __forceinline__ void st_shared_zero16(uint32_t addr) { st_shared_v4(addr, make_uint4(0u, 0u, 0u, 0u)); }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
