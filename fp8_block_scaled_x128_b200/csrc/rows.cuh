@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstdlib>
+#include <cstring>
 #include <mutex>
 
 #include "ptx.cuh"
@@ -334,6 +336,16 @@ inline int sm_count() {
   return n;
 }
 
+// Programmatic dependent launch is on unless FP8G_DISABLE_PDL is set to a nonzero
+// value in the environment (read once), as for the GEMMs.
+inline bool pdl_on() {
+  static const bool on = [] {
+    const char* e = std::getenv("FP8G_DISABLE_PDL");
+    return !(e && *e && std::strcmp(e, "0") != 0);
+  }();
+  return on;
+}
+
 // A launch that may take its place while the kernel before it in the stream
 // still runs (once that one allows it, grid_launch_dependents): it has to wait
 // (grid_dependency_wait) before it reads what that kernel writes.
@@ -347,7 +359,7 @@ inline cudaError_t launch_behind(dim3 grid, int threads, cudaStream_t stream, vo
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = pdl_on() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -539,8 +539,8 @@ def _norm_params(y, post_weight, gate, pre_weight):
     return 2
 
 
-def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=None, eps=1e-6, quantize=False, out=None,
-                  stream=None):
+def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=None, eps=1e-6, quantize=False,
+                  out=None, stream=None):
     """The norms around a block with its gate, residual scale and residual sum:
     h_out = h + scale * gate * post_weight * y / rms(y), z = pre_weight * h_out /
     rms(h_out), rms(x) = sqrt(mean(x^2) + eps) -> (h_out, z), or (h_out, q, sa)
@@ -577,7 +577,7 @@ def norm_residual(y, h=None, post_weight=None, gate=None, scale=1.0, pre_weight=
             _operand(z, y.dtype, (rows, H), dev, "z")
         _operand(h_out, y.dtype, (rows, H), dev, "h_out")
     _check(lib.fp8g_norm_residual(y.data_ptr(), _addr(h), _IN_DTYPE[y.dtype], rows, H, _addr(post_weight),
-                                  _addr(gate), kind, scale, _addr(pre_weight), eps, h_out.data_ptr(), _addr(z),
+                                  _addr(gate), kind, float(scale), _addr(pre_weight), float(eps), h_out.data_ptr(), _addr(z),
                                   _addr(q), _addr(sa), 0 if sa is None else sa.shape[-1], raw),
            "fp8g_norm_residual")
     return (h_out, q, sa) if quantize else (h_out, z)
@@ -601,7 +601,8 @@ def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, sc
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
-            return norm_residual_backward(dz, dh_out, h_out, y, post_weight, gate, scale, pre_weight, eps, out, workspace)
+            return norm_residual_backward(dz, dh_out, h_out, y, post_weight, gate, scale, pre_weight, eps, out,
+                                          workspace)
     raw = _current_raw(dev)
     if out is None:
         dh, dy = torch.empty_like(y), torch.empty_like(y)
@@ -624,7 +625,7 @@ def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, sc
         workspace = torch.empty_strided((need,), (1,), dtype=torch.float32, device=y.device)
     _check(lib.fp8g_norm_residual_backward(_addr(dz), _addr(dh_out), h_out.data_ptr(), y.data_ptr(),
                                            _IN_DTYPE[y.dtype], rows, H, _addr(post_weight), _addr(gate), kind,
-                                           scale, _addr(pre_weight), eps, dh.data_ptr(), dy.data_ptr(), _addr(dpre),
+                                           float(scale), _addr(pre_weight), float(eps), dh.data_ptr(), dy.data_ptr(), _addr(dpre),
                                            _addr(dpost), _addr(dgate), _addr(workspace),
                                            0 if workspace is None else workspace.numel() * 4, raw),
            "fp8g_norm_residual_backward")

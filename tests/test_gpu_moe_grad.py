@@ -267,6 +267,41 @@ def test_dispatch_masked_of_repeated_bad_and_no_experts(g):
     assert p.numel() == 0 and host(m).tolist() == [0, 0, 0]
 
 
+def test_rows_past_32_bit_offsets(g):
+    """Layouts of more than 2^32 bytes and 2^31 elements: the rows at their end."""
+    T, topk, G, N = 34000, 8, 16, 8192
+    e = cuda(routing(4, T, topk, G))
+    x = torch.randn(T, N, device="cuda", dtype=torch.bfloat16)
+    xs, pos, _ = g.moe_permute(x, e, topk, G)
+    assert xs.numel() > 2 ** 31
+    last = torch.arange(T * topk, device="cuda")[-4000:]
+    assert int(pos.max()) * N > 2 ** 31
+    high = torch.topk(pos, 4000).indices                  # the slots in the layout's last rows
+    for sl in (last, high):
+        assert torch.equal(xs[pos[sl].long()], x[sl // topk])
+    w = torch.rand(T * topk, device="cuda")
+    dx = g.moe_permute_backward(xs, pos, T, topk)
+    assert torch.equal(dx[-500:], (x[-500:].float() * topk).to(torch.bfloat16))     # eight equal rows: exact
+    dD, dw = g.moe_combine_backward(x, xs, pos, w, T, topk)
+    assert torch.equal(dD[pos[high].long()], (w[high, None] * x[high // topk].float()).to(torch.bfloat16))
+    want = (x[high // topk].double() ** 2).sum(1)
+    assert bool(((dw[high].double() - want).abs() <= 60 * U * want).all())           # all terms positive
+    del xs, dD, dx
+    torch.cuda.empty_cache()
+    G, Mmax, K = 256, 4200, 4096
+    x = cuda(tokens(2, 9, K), torch.bfloat16)
+    e = torch.tensor([255, 254, 0, 255, 3, 255, 255, 254, 1], dtype=torch.int32, device="cuda")
+    A, sa, p, m = g.moe_dispatch_masked(x, e, 1, G, Mmax)
+    assert A.numel() > 2 ** 32
+    q, s = g.quantize_1x128(x)
+    assert p.tolist() == [255 * Mmax, 254 * Mmax, 0, 255 * Mmax + 1, 3 * Mmax, 255 * Mmax + 2, 255 * Mmax + 3,
+                          254 * Mmax + 1, Mmax]
+    for t in range(9):
+        grp, row = divmod(int(p[t]), Mmax)
+        assert torch.equal(A[grp, row], q[t]) and torch.equal(sa[grp, :, row], s[:, t])
+    assert g.device_error() == 0
+
+
 def bf16_bits(t):
     torch.cuda.synchronize()
     return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)

@@ -280,6 +280,48 @@ def test_calls_at_once_on_two_streams_and_in_two_graphs(g, H):
     assert g.device_error() == 0
 
 
+@pytest.mark.parametrize("H", [8192, 12288])
+def test_rows_past_32_bit_offsets(g, H):
+    """More than 2^31 elements: the rows behind that offset come out as in a call
+    of their own, forward and backward."""
+    rows = 2 ** 31 // H + 300
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    y, h, dz = (torch.empty(rows, H, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    tail = slice(rows - 400, rows)
+    for t in (y, h, dz):
+        t[:400].normal_(generator=gen), t[400:-400].fill_(0.5), t[tail].normal_(generator=gen)
+    w = 1 + 0.2 * torch.randn(H, device="cuda", generator=gen)
+    kw = dict(post_weight=w, scale=0.5, pre_weight=w, eps=EPS)
+    want = g.norm_residual(y[tail].contiguous(), h[tail].contiguous(), **kw)
+    wq = g.norm_residual(y[tail].contiguous(), h[tail].contiguous(), quantize=True, **kw)
+    wb = g.norm_residual_backward(dz[tail].contiguous(), None, h[tail].contiguous(), y[tail].contiguous(), **kw)
+    got = g.norm_residual(y, h, **kw)
+    assert torch.equal(got[0][tail], want[0]) and torch.equal(got[1][tail], want[1])
+    del got
+    _, q, sa = g.norm_residual(y, h, quantize=True, **kw)
+    assert torch.equal(q[tail], wq[1]) and torch.equal(sa[:, tail], wq[2][:, :400])
+    del q, sa
+    dh, dy, _, _, _ = g.norm_residual_backward(dz, None, h, y, **kw)
+    assert torch.equal(dh[tail], wb[0]) and torch.equal(dy[tail], wb[1])
+    del dh, dy, y, h, dz
+    torch.cuda.empty_cache()
+
+
+def test_in_place_wide_rows(g):
+    """h_out over h and z over y where a row takes a cluster of CTAs."""
+    x, gen = inputs(19, 200, 12000, torch.float32, True, "token", True, True)
+    want = call(g, x)
+    y, h = dev(x["y"]), dev(x["h"])
+    kw = dict(post_weight=dev(x["post_w"]), gate=dev(x["gate"]), scale=x["scale"], pre_weight=dev(x["pre_w"]), eps=EPS)
+    g.norm_residual(y, h, out=(h, y), **kw)
+    assert torch.equal(h, want[0]) and torch.equal(y, want[1])
+    dz, dho = (torch.randn(200, 12000, generator=gen).cuda() for _ in range(2))
+    first = g.norm_residual_backward(dz, dho, want[0], dev(x["y"]), **kw)
+    over = dho.clone()
+    g.norm_residual_backward(dz, over, want[0], dev(x["y"]), out=(over, *(torch.empty_like(t) for t in first[1:])), **kw)
+    assert torch.equal(over, first[0])
+
+
 def test_the_same_call_gives_the_same_bits(g):
     x, gen = inputs(12, 1500, 1024, torch.bfloat16, True, "channel", True, True)
     dz = torch.randn(1500, 1024, generator=gen).to(torch.bfloat16).cuda()
