@@ -25,6 +25,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -498,8 +499,8 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) norm_param_grad_kernel(cons
   }
 }
 
-constexpr int kPartsPerSum = 256;  // partial rows of a CTA in the first of two launches
-constexpr int kOneLaunch = 1024;   // up to so many partial rows one launch sums them all
+constexpr int kPartsPerSum = 128;  // partial rows of a CTA in the first of two launches
+constexpr int kOneLaunch = 256;   // up to so many partial rows one launch sums them all
 
 // How a row of H columns is split and how many clusters walk the rows.
 struct Plan {
@@ -522,7 +523,8 @@ constexpr int kNarrow = 2048;
 // kMaxThreads and its stages fit the shared memory; as many CTAs per SM as the
 // registers of `sm_threads` threads and the stages allow.
 Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int vecs, int sm_threads,
-             int kept_one, int kept_cluster) {
+             int kept_one, int kept_cluster,
+             long most_clusters) {
   Plan p{};
   p.vecs = vecs;
   for (p.ctas = 1;; p.ctas *= 2) {
@@ -535,7 +537,7 @@ Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int ve
   const int per_sm = std::max(1, std::min({32, sm_threads / p.threads, kSmemPerSm / p.smem}));
   // no more clusters than rows, and no more than it takes for all to have the
   // same number of rows or one less
-  const long most = std::max(1L, static_cast<long>(kSms) * per_sm / p.ctas);
+  const long most = std::max(1L, std::min(static_cast<long>(kSms) * per_sm / p.ctas, most_clusters));
   const long rounds = std::max(1L, (rows + most - 1) / most);
   p.clusters = std::max(1L, (rows + rounds - 1) / rounds);
   return p;
@@ -547,14 +549,17 @@ Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int ve
 Plan forward_plan(int rows, int H, int dtype) {
   const bool f32 = dtype == FP8G_IN_F32;
   const int vecs = H <= kNarrow ? 1 : 2;
-  return plan_of(rows, H, f32 ? 4 : 2, 2, forward_stages(f32, vecs), H % 128 == 0 ? 128 : 8, vecs, threads_at(64), 32 * vecs, 32 * vecs);
+  return plan_of(rows, H, f32 ? 4 : 2, 2, forward_stages(f32, vecs), H % 128 == 0 ? 128 : 8, vecs, threads_at(64), 32 * vecs, 32 * vecs,
+                 LONG_MAX);
 }
 
+// At least 4 rows a cluster once one launch could not add the partial rows of all
+// (1000 x 512 FP32: 9.2 us against 10.7 with a row each).
 Plan backward_plan(int rows, int H, int dtype) {
   const int vecs = H <= kNarrow ? 1 : 2;
   return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 4, backward_stages(dtype == FP8G_IN_F32, H), 8, vecs,
                  threads_at(backward_regs(dtype == FP8G_IN_F32, vecs)),
-                 32 * vecs, 64 * vecs);
+                 32 * vecs, 64 * vecs, std::max<long>(kOneLaunch, rows / 4));
 }
 
 // Launches the kernel for the plan's cluster size.
