@@ -267,6 +267,29 @@ def test_dispatch_masked_of_repeated_bad_and_no_experts(g):
     assert p.numel() == 0 and host(m).tolist() == [0, 0, 0]
 
 
+def test_long_batches_with_bad_experts(g):
+    """More slots than a warp of the layout kernel keeps in registers, some experts
+    out of range: positions and counts of the oracle, flagged."""
+    T, topk, G = 24000, 4, 37
+    e = routing(6, T, topk, G, 0.01)
+    e[[5, 4000, T * topk - 1]] = [G, -3, 1 << 20]
+    clean = np.where((e < 0) | (e >= G), -1, e).astype(np.int32)
+    x = tokens(3, T, 128)
+    xs, pos, mi = g.moe_permute(cuda(x), cuda(e), topk, G)
+    assert g.device_error() == g.DEVERR_BAD_EXPERT
+    used, cnt, off, wp, wm = oracle.moe_layout(clean, G, mi.numel())
+    assert np.array_equal(host(pos), wp) and np.array_equal(host(mi), wm)
+    live = wp >= 0
+    assert np.array_equal(host(xs)[wp[live]], x[np.nonzero(live)[0] // topk])
+    Mmax = int(np.bincount(clean[clean >= 0], minlength=G).max()) - 5          # some experts overflow
+    A, sa, pos, mm = g.moe_dispatch_masked(cuda(x), cuda(e), topk, G, Mmax)
+    assert g.device_error() == g.DEVERR_BAD_EXPERT | g.DEVERR_MASKED_OVER
+    wp, wm, wq, _, over = masked_reference(x, clean, topk, G, Mmax)
+    assert over and np.array_equal(host(pos), wp) and np.array_equal(host(mm), wm)
+    live = wp >= 0
+    assert np.array_equal(host(A).reshape(G * Mmax, 128)[wp[live]], wq[np.nonzero(live)[0] // topk])
+
+
 def test_rows_past_32_bit_offsets(g):
     """Layouts of more than 2^32 bytes and 2^31 elements: the rows at their end."""
     T, topk, G, N = 34000, 8, 16, 8192
