@@ -45,9 +45,18 @@ constexpr int kMaxH = 16384;
 
 // A row belongs to a cluster of 1, 2 or 4 CTAs, each with a run of its columns;
 // a thread has V vectors of 8 columns, blockDim vectors apart.  The rows stream
-// through shared memory in D stages: a thread copies its own columns of a later
-// row (cp.async) before it works on the current one, so D - 1 rows are under way
-// per CTA, without barriers or waits on other threads.
+// through shared memory in two stages: a thread copies its own columns of a later
+// row (cp.async) while it works on the current one, without barriers or waits on
+// other threads.  More rows under way were slower, not faster (three stages,
+// backward: 8192 x 7168 bf16 118.5 us against 115.5, 8192 x 4096 79 against 74).
+//
+// A row needs a sum before its next row can start, and another one before it
+// can end.  The two are exchanged together: while a row waits for its last sum,
+// the next row's first sums are taken from its stage, which is read again
+// afterwards.  So a row costs one exchange (8192 x 7168 bf16 backward: 131 us
+// with two, 115.5 with one).
+constexpr int kStages = 2;
+
 struct Shape {
   int rows, H;
   int cols;        // columns of a CTA (the last of a cluster may have fewer)
@@ -91,7 +100,7 @@ __device__ __forceinline__ float rms_factor(float sum, float inv_h, float eps) {
 // end, are zeroed once and never copied to, so the arithmetic needs no
 // conditions.  Addresses advance by additions only: with a multiplication per
 // row and tensor, a third of the instructions were address arithmetic.
-template <bool kF32, int V, int kTensors, int D>
+template <bool kF32, int V, int kTensors>
 struct Stream {
   uint32_t slot, pitch, put, get;  // this thread's first slot; stages to fill and to read, as offsets
   long fetch_at;                   // bytes from a tensor's start to this thread's columns of the next row to fetch
@@ -119,7 +128,7 @@ struct Stream {
       for (int i = 0; i < kTensors; ++i) {
         if (in[v] && t[i]) continue;
 #pragma unroll
-        for (int s = 0; s < D; ++s) {
+        for (int s = 0; s < kStages; ++s) {
           const uint32_t at = slot + (s * kTensors + i) * pitch + v * apart();
           st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
           if constexpr (kF32) st_shared_v4(at + 16, make_uint4(0u, 0u, 0u, 0u));
@@ -144,14 +153,14 @@ struct Stream {
     cp_commit();
     --left;
     fetch_at += step_bytes;
-    put = put == (D - 1) * kTensors * pitch ? 0 : put + kTensors * pitch;
+    put = put == (kStages - 1) * kTensors * pitch ? 0 : put + kTensors * pitch;
   }
 
   __device__ __forceinline__ Pair8 load(int tensor, int v) const {
     return pairs_of<kF32>(load8_shared<kF32>(slot + get + tensor * pitch + v * apart()));
   }
 
-  __device__ __forceinline__ void advance() { get = get == (D - 1) * kTensors * pitch ? 0 : get + kTensors * pitch; }
+  __device__ __forceinline__ void advance() { get = get == (kStages - 1) * kTensors * pitch ? 0 : get + kTensors * pitch; }
 };
 
 // Stores a thread's 8 values of a row, rounded once.
@@ -178,47 +187,44 @@ __device__ __forceinline__ void leave_together() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Stages: two where two CTAs share an SM (bf16, two vectors a thread), else three.
-__host__ __device__ constexpr int forward_stages(bool f32, int vecs) { return !f32 && vecs == 2 ? 2 : 3; }
-// The backward pass: three for bf16 rows of one CTA, two where three do not fit.
-constexpr int kOneCta = 8192;  // columns of bf16 that one CTA takes
-constexpr int backward_stages(bool f32, int H) { return f32 || H > kOneCta ? 2 : 3; }
-
 // Most threads of a CTA, and the registers a thread of the backward kernel may
 // use (the forward kernel: 64).  They leave nothing to be kept in local memory:
 // with the stages in shared memory the L1 cache has a few KB, and six words
-// spilled cost 8192 x 7168 180 us instead of 131.
+// spilled cost 8192 x 7168 some 50 us.
 constexpr int kMaxThreads = 512;
 constexpr int backward_regs(bool f32, int vecs) { return vecs == 2 ? 128 : f32 ? 88 : 80; }
 // Threads of an SM whose registers fit: each of its four parts has 16384.
 constexpr int threads_at(int regs) { return 128 * (16384 / (32 * regs)); }
 
 // Forward.  Each element of y and h is read once and each of h' and z written
-// once.  8192 x 7168 bf16 with post-norm and channel gate: 79.5 us, 5.9 TB/s, 0.90
-// of the measured copy bandwidth (32768 x 1024: 46 us, 0.89; 4096 x 16384: 104 us,
-// 0.79); two CTAs share an SM, so that one computes while the other waits for a
-// sum.  With codes out 89 us, 0.71: the quantisation adds a third to the
-// instructions, and the issue slots (57 %) and the sums' latency bound it.  One
-// row of 7168, decode's form: 4.1 us, two sums' latencies behind one load.
+// once.  8192 x 7168 bf16 with post-norm and channel gate: 76.7 us, 6.1 TB/s, 0.93
+// of the measured copy bandwidth (32768 x 1024: 45.5 us, 0.90; 4096 x 16384: 89 us,
+// 0.92); two CTAs share an SM, so that one computes while the other waits for a
+// sum.  With codes out 84 us, 0.75: the quantisation adds a third to the
+// instructions, and the issue slots and the sum's latency bound it.  One row of
+// 7168, decode's form: 4.2 us, two sums' latencies behind one load.
 template <bool kF32, int V, int kC, bool kQuant>
 __global__ void __launch_bounds__(kMaxThreads, 2)
     norm_residual_kernel(const void* y, const void* h, Shape S, Params P, void* h_out, void* z, uint8_t* q, float* sa,
                          int ld_sa, uint32_t* err) {
   extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ RowSum<1, kC> sm_y, sm_h;
-  constexpr int D = forward_stages(kF32, V);
-  row_sum_init(sm_y), row_sum_init(sm_h);
+  __shared__ RowSum<2, kC> sm;
+  // The next copies are issued behind the row's sum, before its output, and for
+  // narrow bf16 rows before the sum (8192 x 7168 76.7 us against 87, 32768 x 1024
+  // 50.2 against 45.5; 16384 x 1024 FP32 48.1 against 51)
+  constexpr bool kLate = kF32 || V == 2;
+  row_sum_init(sm);
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
   const int col0 = rank * S.cols;
   const void* const tensors[2] = {y, h};
-  Stream<kF32, V, 2, D> src;
+  Stream<kF32, V, 2> src;
   src.init(tensors, dyn, S, col0, row0, step);
   long at = src.fetch_at;  // this thread's columns of the current row
 #pragma unroll
-  for (int s = 0; s < D - 1; ++s) src.fetch(tensors, 1);
+  for (int s = 0; s < kStages; ++s) src.fetch(tensors, 1);
   // post_w (g per channel) stays in shared memory, pre_w in registers
-  const uint32_t a_at = fp8g::smem_u32(dyn) + 2 * D * S.pitch + threadIdx.x * 32;
+  const uint32_t a_at = fp8g::smem_u32(dyn) + 2 * kStages * S.pitch + threadIdx.x * 32;
   Pair8 pw[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -230,41 +236,56 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   const float inv_h = 1.f / static_cast<float>(S.H);
   bool gave_up = false;
   unsigned it = 0;
-  for (long row = row0; row < S.rows; row += step, ++it) {
-    const float gt = P.gate_kind == FP8G_GATE_TOKEN ? __ldg(P.gate + row) : 1.f;  // used behind the first sum
-    src.fetch(tensors, 1);
-    cp_wait<D - 1>();
-    Pair8 yv[V], hv[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) yv[v] = src.load(0, v), hv[v] = src.load(1, v);
-    src.advance();
-    float f = P.scale, ss[1];
-    if (P.post_w) {
-      uint64_t acc = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc = fma2(yv[v].v[i], yv[v].v[i], acc);
-      ss[0] = sum2(acc);
-      row_sum(ss, sm_y, it, rank, gave_up, err);
-      f *= rms_factor(ss[0], inv_h, P.eps);
-    }
-    uint64_t acc = 0;
-    const uint64_t ff = both(f * gt);
+  float st[2] = {};  // y^2 of the next row, h'^2 of the current one
+  auto statistics = [&] {
+    uint64_t yy = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const Pair8 a = kept8(a_at + v * blockDim.x * 32);
+      const Pair8 yv = src.load(0, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) yy = fma2(yv.v[i], yv.v[i], yy);
+    }
+    st[0] = sum2(yy);
+  };
+  const bool token = P.gate_kind == FP8G_GATE_TOKEN;
+  auto next_row = [&] {
+    cp_wait<kLate ? 0 : 1>();
+    src.advance();
+  };
+  cp_wait<1>();
+  if (P.post_w) {
+    statistics();
+    row_sum(st, sm, it++, rank, gave_up, err);
+  }
+  for (long row = row0; row < S.rows; row += step, ++it) {
+    float f = token ? P.scale * __ldg(P.gate + row) : P.scale;
+    if (P.post_w) f *= rms_factor(st[0], inv_h, P.eps);
+    const uint64_t ff = both(f);
+    uint64_t acc = 0;
+    Pair8 hv[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      hv[v] = src.load(1, v);
+      const Pair8 yv = src.load(0, v), a = kept8(a_at + v * blockDim.x * 32);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        hv[v].v[i] = fma2(a.v[i], mul2(yv[v].v[i], ff), hv[v].v[i]);
+        hv[v].v[i] = fma2(a.v[i], mul2(yv.v[i], ff), hv[v].v[i]);
         acc = fma2(hv[v].v[i], hv[v].v[i], acc);
       }
       if (src.in[v]) put8<kF32>(h_out, at + v * src.apart(), hv[v]);
     }
-    ss[0] = sum2(acc);
-    row_sum(ss, sm_h, it, rank, gave_up, err);
+    // this stage is free; the next row's sum shares the exchange of this row's
+    if constexpr (!kLate) src.fetch(tensors, 1);
+    if (P.post_w) {
+      next_row();
+      if (row + step < S.rows) statistics();
+    }
+    st[1] = sum2(acc);
+    row_sum(st, sm, it, rank, gave_up, err);
+    if (!P.post_w) next_row();
+    if constexpr (kLate) src.fetch(tensors, 1);
     // the quantiser takes the negatives of its values
-    const float r = rms_factor(ss[0], inv_h, P.eps);
+    const float r = rms_factor(st[1], inv_h, P.eps);
     const uint64_t r1 = both(kQuant ? -r : r);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -303,131 +324,105 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
 // atomics: the same bits every run).  Those sums belong to columns, so a thread
 // has to keep its columns for all rows, and a row takes the whole CTA.
 //
-// dy needs a sum over the row of a dh u, and dh the row's statistics.  One CTA
-// takes two sums one after the other.  A cluster, where each costs several
-// times as much, puts the second together from sums that do not need dh (dh is
-// dh_out + r1 dn - r1 <dn n> n), so a row takes one; the extra products and
-// reads of shared memory made a single CTA slower (8192 x 7168 bf16: 150 us
-// against 132).
+// dh needs the row's statistics, and dy a sum over the row of a dh u, which is
+// exchanged with the next row's statistics.
 //
-// 8192 x 7168 bf16: 131 us with the parameter sums, 5.4 TB/s, 0.82 of the measured
-// copy bandwidth; 14 warps an SM at 128 registers, 48 % of the issue slots, the
-// rest waits for the two sums.  32768 x 1024: 84 us (0.73, instructions issued);
-// 4096 x 16384: 201 us (0.61) and 4096 x 7168 FP32 149 us (0.72), shared memory
-// and the clusters' sums.
-template <bool kF32, int V, int D, int kC>
+// 8192 x 7168 bf16: 115.5 us with the parameter sums, 6.1 TB/s, 0.93 of the measured
+// copy bandwidth (8192 x 8192: 131 us, 0.94; 32768 x 1024: 76 us, 0.81; 4096 x 16384:
+// 144 us, 0.86; 4096 x 7168 FP32: 131 us, 0.82), at 14 warps an SM of 128 registers.
+// Narrower rows are bound by instructions issued, a few rows by the launches and
+// the latency of load, sum and store (400 x 2112 FP32: 12.9 us).
+template <bool kF32, int V, int kC>
 __global__ void __maxnreg__(backward_regs(kF32, V))
     norm_residual_backward_kernel(const void* dz, const void* dh_out, const void* h, const void* y, Shape S, Params P,
                                   void* dh, void* dy, float* __restrict__ dgate, float* __restrict__ part, uint32_t* err) {
-  constexpr bool kOneSum = kC > 1;
   extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ RowSum<kOneSum ? 8 : 4, kC> sm;
-  __shared__ RowSum<1, 1> sm_dot;
+  __shared__ RowSum<4, kC> sm;
   row_sum_init(sm);
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
   const int col0 = rank * S.cols;
   const void* const tensors[4] = {h, y, dz, dh_out};
-  Stream<kF32, V, 4, D> src;
+  Stream<kF32, V, 4> src;
   src.init(tensors, dyn, S, col0, row0, step);
   long at = src.fetch_at;
 #pragma unroll
-  for (int s = 0; s < D - 1; ++s) src.fetch(tensors, 2);
-  // a = s post_w (g per channel) stays in shared memory, the sums in registers,
-  // and so does pre_w where there is room
-  const uint32_t a_at = fp8g::smem_u32(dyn) + 4 * D * S.pitch + threadIdx.x * 32;
-  const uint32_t pre_at = a_at + V * blockDim.x * 32;
-  Pair8 pre_reg[kOneSum ? 1 : V], acc_pre[V] = {}, acc_u[V] = {};
+  for (int s = 0; s < kStages; ++s) src.fetch(tensors, 2);
+  // a = s post_w (g per channel) stays in shared memory, pre_w and the sums in registers
+  const uint32_t a_at = fp8g::smem_u32(dyn) + 4 * kStages * S.pitch + threadIdx.x * 32;
+  Pair8 pre[V], acc_pre[V] = {}, acc_u[V] = {};
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    Pair8 a, pw;
-    column_params(P, col0 + 8 * (threadIdx.x + v * blockDim.x), src.in[v], pw, a);
+    Pair8 a;
+    column_params(P, col0 + 8 * (threadIdx.x + v * blockDim.x), src.in[v], pre[v], a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) a.v[i] = mul2(a.v[i], both(P.scale));
     keep8(a_at + v * blockDim.x * 32, a);
-    if constexpr (kOneSum) keep8(pre_at + v * blockDim.x * 32, pw);
-    else pre_reg[v] = pw;
   }
-  auto pre = [&](int v) {
-    if constexpr (kOneSum) return kept8(pre_at + v * blockDim.x * 32);
-    else return pre_reg[v];
-  };
   if constexpr (kC > 1) cluster_sync_all();
   if (threadIdx.x == 0) fp8g::grid_launch_dependents();  // the kernel that adds the partial rows waits for this one
   const float inv_h = 1.f / static_cast<float>(S.H);
   const bool token = P.gate_kind == FP8G_GATE_TOKEN;
   bool gave_up = false;
   unsigned it = 0;
-  for (long row = row0; row < S.rows; row += step, ++it) {
-    src.fetch(tensors, 2);
-    cp_wait<D - 1>();
-    Pair8 hv[V], yv[V], g[V];  // g: dz, then dh, then du
-    // h'^2, dn h', y^2 with dn = dz pre_w; and a y dh_out, a y dn, a y h'
-    uint64_t hh = 0, nh = 0, yy = 0, ad = 0, an = 0, ah = 0;
+  float st[4] = {};  // h'^2, dn h', y^2 of the next row, with dn = dz pre_w; a dh u of the current one
+  auto statistics = [&] {
+    uint64_t hh = 0, nh = 0, yy = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      hv[v] = src.load(0, v), yv[v] = src.load(1, v), g[v] = src.load(2, v);
-      const Pair8 pw = pre(v);
-      Pair8 d = {}, a = {};
-      if constexpr (kOneSum) d = src.load(3, v), a = kept8(a_at + v * blockDim.x * 32);
+      const Pair8 hv = src.load(0, v), yv = src.load(1, v), z = src.load(2, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint64_t n = mul2(g[v].v[i], pw.v[i]);
-        hh = fma2(hv[v].v[i], hv[v].v[i], hh);
-        nh = fma2(n, hv[v].v[i], nh);
-        yy = fma2(yv[v].v[i], yv[v].v[i], yy);
-        if constexpr (kOneSum) {
-          const uint64_t ay = mul2(a.v[i], yv[v].v[i]);
-          ad = fma2(ay, d.v[i], ad);
-          an = fma2(ay, n, an);
-          ah = fma2(ay, hv[v].v[i], ah);
-        }
+        hh = fma2(hv.v[i], hv.v[i], hh);
+        nh = fma2(mul2(z.v[i], pre[v].v[i]), hv.v[i], nh);
+        yy = fma2(yv.v[i], yv.v[i], yy);
       }
     }
-    float st[kOneSum ? 8 : 4] = {sum2(hh), sum2(nh), sum2(yy)};
-    if constexpr (kOneSum) st[3] = sum2(ad), st[4] = sum2(an), st[5] = sum2(ah);
-    row_sum(st, sm, it, rank, gave_up, err);
+    st[0] = sum2(hh), st[1] = sum2(nh), st[2] = sum2(yy);
+  };
+  cp_wait<1>();
+  statistics();
+  row_sum(st, sm, it++, rank, gave_up, err);
+  for (long row = row0; row < S.rows; row += step, ++it) {
     const float gt = token ? __ldg(P.gate + row) : 1.f;
     const float r1 = rms_factor(st[0], inv_h, P.eps);
     const float r2 = P.post_w ? rms_factor(st[2], inv_h, P.eps) : 1.f;
-    const float m1 = -r1 * (st[1] * r1 * inv_h);  // - r1 <dn n>, n = h' r1
-    const uint64_t rr1 = both(r1), rr2 = both(r2), rm = both(m1);
+    const uint64_t rr1 = both(r1), rr2 = both(r2), rm = both(-r1 * (st[1] * r1 * inv_h));  // - r1 <dn n>, n = h' r1
+    Pair8 u[V], g[V];  // g: dh, then a dh
     uint64_t du_u = 0;  // a dh u
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const Pair8 d = src.load(3, v), pw = pre(v);
+      const Pair8 hv = src.load(0, v), yv = src.load(1, v), z = src.load(2, v), d = src.load(3, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint64_t n = mul2(hv[v].v[i], rr1);
-        acc_pre[v].v[i] = fma2(g[v].v[i], n, acc_pre[v].v[i]);
-        g[v].v[i] = fma2(n, rm, fma2(mul2(g[v].v[i], pw.v[i]), rr1, d.v[i]));
+        const uint64_t n = mul2(hv.v[i], rr1);
+        acc_pre[v].v[i] = fma2(z.v[i], n, acc_pre[v].v[i]);
+        g[v].v[i] = fma2(n, rm, fma2(mul2(z.v[i], pre[v].v[i]), rr1, d.v[i]));
       }
       if (src.in[v]) put8<kF32>(dh, at + v * src.apart(), g[v]);
       const Pair8 a = kept8(a_at + v * blockDim.x * 32);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        yv[v].v[i] = mul2(yv[v].v[i], rr2);
-        acc_u[v].v[i] = fma2(token ? mul2(g[v].v[i], both(gt)) : g[v].v[i], yv[v].v[i], acc_u[v].v[i]);
+        u[v].v[i] = mul2(yv.v[i], rr2);
+        acc_u[v].v[i] = fma2(token ? mul2(g[v].v[i], both(gt)) : g[v].v[i], u[v].v[i], acc_u[v].v[i]);
         g[v].v[i] = mul2(g[v].v[i], a.v[i]);
-        if constexpr (!kOneSum) du_u = fma2(g[v].v[i], yv[v].v[i], du_u);
+        du_u = fma2(g[v].v[i], u[v].v[i], du_u);
       }
     }
+    // this stage is free; the next row's statistics share the exchange of this row's sum
+    src.fetch(tensors, 2);
+    cp_wait<1>();
     src.advance();
-    float dot = 0.f;
-    if constexpr (kOneSum) {
-      dot = r2 * fmaf(m1 * r1, st[5], fmaf(r1, st[4], st[3]));
-    } else if (P.post_w || token) {
-      float s1[1] = {sum2(du_u)};
-      row_sum(s1, sm_dot, it, rank, gave_up, err);
-      dot = s1[0];
-    }
-    const float m2 = P.post_w ? dot * gt * inv_h : 0.f;  // <du u>
-    if (dgate && token && rank == 0 && threadIdx.x == 0) dgate[row] = dot;
+    if (row + step < S.rows) statistics();
+    st[3] = sum2(du_u);
+    row_sum(st, sm, it, rank, gave_up, err);
+    const float m2 = P.post_w ? st[3] * gt * inv_h : 0.f;  // <du u>
+    if (dgate && token && rank == 0 && threadIdx.x == 0) dgate[row] = st[3];
     const uint64_t f = both(r2 * gt), um = both(-r2 * m2);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) g[v].v[i] = fma2(g[v].v[i], f, mul2(yv[v].v[i], um));
+      for (int i = 0; i < 4; ++i) g[v].v[i] = fma2(g[v].v[i], f, mul2(u[v].v[i], um));
       if (src.in[v]) put8<kF32>(dy, at + v * src.apart(), g[v]);
     }
     at += src.step_bytes;
@@ -513,25 +508,23 @@ struct Plan {
 };
 
 constexpr int kSms = 148;
-constexpr int kSmemPerSm = 224 << 10;  // of 227 KB: the static part takes up to 5 KB where the stages leave more
-// Rows up to so many columns get one vector a thread, wider ones two: half the
-// warps carry the per-row work (8192 x 4096 bf16 backward 104 us with one vector,
-// 72 with two; 8192 x 3000 forward 45 and 37).
+constexpr int kSmemPerSm = 224 << 10;  // of 227 KB: the static part takes up to 2.2 KB
+// Rows up to so many columns get one vector a thread, wider ones two, so that half
+// the warps carry the per-row work (backward of 8192 x 3000 bf16 64 us with one
+// vector, 59 with two; forward of 8192 x 2048 FP32 45 us with one, 48 with two).
 constexpr int kNarrow = 2048;
 
 // tensors: rows streamed per stage.  The cluster grows until a CTA has at most
 // kMaxThreads and its stages fit the shared memory; as many CTAs per SM as the
 // registers of `sm_threads` threads and the stages allow.
-Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int vecs, int sm_threads,
-             int kept_one, int kept_cluster,
-             long most_clusters) {
+Plan plan_of(int rows, int H, int esz, int tensors, int unit, int vecs, int sm_threads, long most_clusters) {
   Plan p{};
   p.vecs = vecs;
   for (p.ctas = 1;; p.ctas *= 2) {
     const int cols = ((H + unit - 1) / unit + p.ctas - 1) / p.ctas * unit;
     p.threads = (cols / 8 + 32 * vecs - 1) / (32 * vecs) * 32;
     p.S = Shape{rows, H, cols, static_cast<uint32_t>(p.threads * vecs * 8 * esz)};
-    p.smem = tensors * stages * static_cast<int>(p.S.pitch) + (p.ctas == 1 ? kept_one : kept_cluster) * p.threads;
+    p.smem = tensors * kStages * static_cast<int>(p.S.pitch) + 32 * vecs * p.threads;
     if (p.ctas == 4 || (p.threads <= std::min(kMaxThreads, sm_threads) && p.smem <= kSmemPerSm)) break;
   }
   const int per_sm = std::max(1, std::min({32, sm_threads / p.threads, kSmemPerSm / p.smem}));
@@ -549,17 +542,16 @@ Plan plan_of(int rows, int H, int esz, int tensors, int stages, int unit, int ve
 Plan forward_plan(int rows, int H, int dtype) {
   const bool f32 = dtype == FP8G_IN_F32;
   const int vecs = H <= kNarrow ? 1 : 2;
-  return plan_of(rows, H, f32 ? 4 : 2, 2, forward_stages(f32, vecs), H % 128 == 0 ? 128 : 8, vecs, threads_at(64), 32 * vecs, 32 * vecs,
-                 LONG_MAX);
+  return plan_of(rows, H, f32 ? 4 : 2, 2, H % 128 == 0 ? 128 : 8, vecs, threads_at(64), LONG_MAX);
 }
 
 // At least 4 rows a cluster once one launch could not add the partial rows of all
 // (1000 x 512 FP32: 9.2 us against 10.7 with a row each).
 Plan backward_plan(int rows, int H, int dtype) {
   const int vecs = H <= kNarrow ? 1 : 2;
-  return plan_of(rows, H, dtype == FP8G_IN_F32 ? 4 : 2, 4, backward_stages(dtype == FP8G_IN_F32, H), 8, vecs,
-                 threads_at(backward_regs(dtype == FP8G_IN_F32, vecs)),
-                 32 * vecs, 64 * vecs, std::max<long>(kOneLaunch, rows / 4));
+  const bool f32 = dtype == FP8G_IN_F32;
+  return plan_of(rows, H, f32 ? 4 : 2, 4, 8, vecs, threads_at(backward_regs(f32, vecs)),
+                 std::max<long>(kOneLaunch, rows / 4));
 }
 
 // Launches the kernel for the plan's cluster size.
@@ -671,15 +663,15 @@ extern "C" int fp8g_norm_residual_backward(const void* dz, const void* dh_out, c
   if (rows > 0) {
     auto go = [&](auto kernel) { return launch(p, kernel, stream, dz, dh_out, h_out, y, p.S, P, dh, dy, dgate, part, err); };
     cudaError_t e;
-    if (dtype == FP8G_IN_F32)  // 1 CTA up to 5600 columns, 2 up to 11264
-      e = p.vecs == 1   ? go(norm_residual_backward_kernel<true, 1, 2, 1>)
-          : p.ctas == 1 ? go(norm_residual_backward_kernel<true, 2, 2, 1>)
-          : p.ctas == 2 ? go(norm_residual_backward_kernel<true, 2, 2, 2>)
-                        : go(norm_residual_backward_kernel<true, 2, 2, 4>);
+    if (dtype == FP8G_IN_F32)  // 1 CTA up to 6144 columns, 2 up to 12288
+      e = p.vecs == 1   ? go(norm_residual_backward_kernel<true, 1, 1>)
+          : p.ctas == 1 ? go(norm_residual_backward_kernel<true, 2, 1>)
+          : p.ctas == 2 ? go(norm_residual_backward_kernel<true, 2, 2>)
+                        : go(norm_residual_backward_kernel<true, 2, 4>);
     else  // 1 CTA up to 8192 columns, 2 above
-      e = p.vecs == 1   ? go(norm_residual_backward_kernel<false, 1, 3, 1>)
-          : p.ctas == 1 ? go(norm_residual_backward_kernel<false, 2, 3, 1>)
-                        : go(norm_residual_backward_kernel<false, 2, 2, 2>);
+      e = p.vecs == 1   ? go(norm_residual_backward_kernel<false, 1, 1>)
+          : p.ctas == 1 ? go(norm_residual_backward_kernel<false, 2, 1>)
+                        : go(norm_residual_backward_kernel<false, 2, 2>);
     if (e != cudaSuccess) {
       (void)cudaGetLastError();
       return FP8G_ERR_CUDA;

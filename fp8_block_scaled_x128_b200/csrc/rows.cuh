@@ -134,8 +134,8 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// Four (eight) sums over a warp in 6 (9) shuffles instead of 20 (40): the first
-// steps halve the values a lane carries, so the lanes of octet (quad) o end with
+// Four (two) sums over a warp in 6 (5) shuffles instead of 20 (10): the first
+// steps halve the values a lane carries, so the lanes of octet (half) o end with
 // the sum of v[o].
 __device__ __forceinline__ float warp_sums(const float (&v)[4]) {
   const int lane = threadIdx.x & 31;
@@ -150,24 +150,15 @@ __device__ __forceinline__ float warp_sums(const float (&v)[4]) {
   return x;
 }
 
-__device__ __forceinline__ float warp_sums(const float (&v)[8]) {
-  const int lane = threadIdx.x & 31;
-  const bool b16 = lane & 16, b8 = lane & 8, b4 = lane & 4;
-  float a[4], c[2], x;
+__device__ __forceinline__ float warp_sums(const float (&v)[2]) {
+  const bool b16 = threadIdx.x & 16;
+  float x = (b16 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, b16 ? v[0] : v[1], 16);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    a[i] = (b16 ? v[4 + i] : v[i]) + __shfl_xor_sync(0xffffffffu, b16 ? v[i] : v[4 + i], 16);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    c[i] = (b8 ? a[2 + i] : a[i]) + __shfl_xor_sync(0xffffffffu, b8 ? a[i] : a[2 + i], 8);
-  x = (b4 ? c[1] : c[0]) + __shfl_xor_sync(0xffffffffu, b4 ? c[0] : c[1], 4);
-  x += __shfl_xor_sync(0xffffffffu, x, 2);
-  return x + __shfl_xor_sync(0xffffffffu, x, 1);
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
-__device__ __forceinline__ float warp_sums(const float (&v)[1]) { return warp_sum(v[0]); }
-
-// Sums of n (1, 4 or 8) values over the kC CTAs of a cluster, in every thread, in
+// Sums of n (2 or 4) values over the kC CTAs of a cluster, in every thread, in
 // a fixed order that gives every thread the same bits.  At most 16 warps a CTA;
 // `call` counts the calls on this sm from 0.
 //
@@ -179,11 +170,10 @@ __device__ __forceinline__ float warp_sums(const float (&v)[1]) { return warp_su
 // A cluster: each warp sends its sums into every CTA's shared memory (st.async),
 // and a CTA waits until all of them have arrived on its own mbarrier.  A cluster
 // barrier instead would order, and so wait for, the rows the threads have just
-// stored to global memory (backward of 4096 x 7168 FP32: 182 us with cluster
-// barriers, 149 without).  A CTA writes a
-// peer's buffer again only after it has the peer's sums of the call in between,
-// which every warp of the peer sends after reading the buffer; and it leaves
-// after all sums sent to it have arrived.
+// stored to global memory (it cost the backward of 4096 x 7168 FP32 33 us).  A CTA
+// writes a peer's buffer again only after it has the peer's sums of the call in
+// between, which every warp of the peer sends after reading the buffer; and it
+// leaves after all sums sent to it have arrived.
 template <int n, int kC>
 struct RowSum {
   float s[2][n][16 * kC];
@@ -242,14 +232,14 @@ __device__ __forceinline__ void row_sum(float (&v)[n], RowSum<n, kC>& sm, unsign
 #pragma unroll
     for (int c = 0; c < kC; ++c)
 #pragma unroll
-      for (int i = 0; i < (kLanes >= 16 ? 1 : 16 / kLanes); ++i)
-        x += peer + kLanes * i < nw ? sm.s[turn][value][16 * c + (kLanes >= 16 ? peer & 15 : peer + kLanes * i)] : 0.f;
+      for (int i = 0; i < 16 / kLanes; ++i)
+        x += peer + kLanes * i < nw ? sm.s[turn][value][16 * c + peer + kLanes * i] : 0.f;
 #pragma unroll
-    for (int o = kLanes > 16 ? 8 : kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     mine = x;
   }
 #pragma unroll
-  for (int i = 0; i < n; ++i) v[i] = n == 1 && kC == 1 && nw == 1 ? mine : __shfl_sync(0xffffffffu, mine, kLanes * i);
+  for (int i = 0; i < n; ++i) v[i] = __shfl_sync(0xffffffffu, mine, kLanes * i);
 }
 
 // ---------------------------------------------------------------- asynchronous copies

@@ -240,6 +240,38 @@ def test_in_place_streams_and_graphs(g):
     assert torch.equal(over, second[0])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [128, 1152, 2112, 6152, 8192, 8320, 12416, 16384])
+@pytest.mark.parametrize("post,gate", [(True, "token"), (False, "token"), (True, "channel"), (False, "none")])
+def test_a_row_comes_out_alike_wherever_it_stands(g, H, post, gate, dtype):
+    """Many rows a CTA or cluster, one after the other, give what each row gives
+    in a call of few rows (a row each): every row's sums run in one order.  The
+    first row of a CTA, its last ones and rows behind an infinite one included."""
+    rows, part = 2 * 148 * 4 + 5 if H < 4096 else 601, 60
+    x, gen = inputs(H, rows, H, dtype, post, gate, True, True)
+    dz, dho = (torch.randn(rows, H, generator=gen).to(dtype).cuda() for _ in range(2))
+    y, h, gt, w, pw = (dev(x[n]) for n in ("y", "h", "gate", "post_w", "pre_w"))
+    y[11, 3] = float("inf")
+
+    def run(at):
+        kw = dict(post_weight=w, scale=x["scale"], pre_weight=pw, eps=EPS, gate=gt[at].contiguous() if gate == "token" else gt)
+        h_out, z = g.norm_residual(y[at], h[at], **kw)
+        dh, dy, _, _, dg = g.norm_residual_backward(dz[at], dho[at], h[at], y[at], **kw)
+        out = [h_out, z, dh, dy] + ([dg] if gate == "token" else [])
+        if H % 128 == 0:
+            _, q, sa = g.norm_residual(y[at], h[at], quantize=True, **kw)
+            out += [q, sa[:, :q.shape[0]].t()]
+        return out
+
+    bits = lambda t: t.contiguous().view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()])
+    whole, clean = run(slice(None)), torch.arange(rows) != 11
+    for r in (0, 300, rows - part):
+        few = run(slice(r, r + part))
+        for i, (a, b) in enumerate(zip(whole, few)):
+            assert torch.equal(bits(a[r:r + part])[clean[r:r + part]], bits(b)[clean[r:r + part]]), (r, i)
+    assert g.device_error() == 0
+
+
 @pytest.mark.parametrize("H", [256, 7168, 12000])
 def test_calls_at_once_on_two_streams_and_in_two_graphs(g, H):
     """Two backward passes under way together, each with the workspace it makes
