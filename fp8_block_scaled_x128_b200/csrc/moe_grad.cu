@@ -6,9 +6,9 @@
 //   combine backward   of out[t] = sum_k w[r] D[pos[r]]:
 //                      dD[pos[r]] = w[r] dout[t], dw[r] = <dout[t], D[pos[r]]>
 //
-// All three are HBM-bound streams.  A CTA takes a token: its row of x or dout
-// is read once for all of its slots, and every row of the layout is touched
-// once.  Positions are checked against the layout's rows before any access; a
+// All three are HBM-bound streams.  A CTA takes a token (several, where rows are
+// narrow and tokens many): its row of x or dout is read once for all of its
+// slots, and every row of the layout is touched once.  Positions are checked against the layout's rows before any access; a
 // position outside is flagged and its slot skipped.
 //
 // Padding rows.  The rows of a used block (one that holds a routed row) that
@@ -106,11 +106,11 @@ __device__ __forceinline__ void pad_range(int cta, int pads, int blocks, int& b0
 // each, one 16-byte vector a thread, whatever the type: short CTAs leave little
 // work behind when the last ones run (with a CTA per token, 3.5 waves of 8 CTAs
 // an SM, the last wave ran half empty).  4096 tokens x top-8 over 64 experts, 7168
-// bf16: 103 us with the layout kernel (of which some 7 us are not hidden), 588 MB
-// with the padding rows: 0.87 of the measured copy bandwidth.
+// bf16: 101 us with the layout kernel (of which some 7 us are not hidden), 588 MB
+// with the padding rows: 0.89 of the measured copy bandwidth.
 template <int kCap>
-__global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int parts, int T, int topk,
-                                                          const int32_t* __restrict__ pos, uint4* __restrict__ xs, int M,
+__global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int parts, int tokens, int T,
+                                                          int topk, const int32_t* __restrict__ pos, uint4* __restrict__ xs, int M,
                                                           int blocks, int pads, uint32_t* err) {
   __shared__ uint32_t bits[kPadBlocks * 4];
   if (static_cast<int>(blockIdx.x) < pads) {
@@ -122,26 +122,30 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restric
     });
     return;
   }
-  const long items = static_cast<long>(T) * parts;
-  long i = static_cast<long>(blockIdx.x) - pads;
-  auto vector_of = [&](long item) {  // this thread's vector of an item, -1 behind the row's end
-    const long t = item / parts;
-    const int j = static_cast<int>(item - t * parts) * blockDim.x + threadIdx.x;
-    return j < vecs ? t * vecs + j : -1L;
+  const int row_threads = blockDim.x / tokens, sub = threadIdx.x / row_threads, tid = threadIdx.x - sub * row_threads;
+  // an item is a part of a token's row, or `tokens` short rows; memory holds fewer than 2^32 of them
+  const unsigned items = (static_cast<unsigned>(T) + tokens - 1) / tokens * parts, stride = gridDim.x - pads;
+  long t, at;  // of the current item: this thread's token, and its vector or -1 behind the row's end or the last token
+  auto locate = [&](unsigned item) {
+    const unsigned first = item / parts;
+    const int j = static_cast<int>(item - first * parts) * row_threads + tid;
+    t = static_cast<long>(first) * tokens + sub;
+    at = j < vecs && t < T ? t * vecs + j : -1L;
   };
-  long at = i < items ? vector_of(i) : -1;
+  unsigned i = blockIdx.x - pads;
+  locate(i);
   uint4 v = at >= 0 ? __ldcs(x + at) : make_uint4(0u, 0u, 0u, 0u);  // x does not come from the layout kernel
   fp8g::grid_dependency_wait();                                     // pos does
   while (i < items) {
-    const long t = i / parts, j = at - t * vecs;
+    const long j = at - t * vecs;
 #pragma unroll
     for (int k = 0; k < kCap; ++k) {
-      const int p = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+      const int p = k < topk && t < T ? checked_pos(pos, t * topk + k, M, err) : -1;
       if (p >= 0 && at >= 0) __stcs(xs + static_cast<long>(p) * vecs + j, v);
     }
-    i += static_cast<long>(gridDim.x) - pads;
+    i += stride;
     if (i < items) {
-      at = vector_of(i);
+      locate(i);
       if (at >= 0) v = __ldcs(x + at);
     }
   }
@@ -258,8 +262,8 @@ __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* _
 // a thread), four slots at a time.  A thread copies its own vectors of the next
 // four slots' D rows (and of dout) into shared memory (cp.async) before it works
 // on the current ones, so loads are under way all the time without holding
-// registers.  The same rows, 1.06 GB with the padding: 176 us to bf16, 0.92 of the
-// measured copy bandwidth; 0.80 GB to codes: 147 us, 0.83, with 60 % of the issue
+// registers.  The same rows, 1.06 GB with the padding: 171 us to bf16, 0.94 of the
+// measured copy bandwidth; 0.80 GB to codes: 141 us, 0.86, with 60 % of the issue
 // slots used (packed FP32x2 arithmetic throughout).
 //
 // kQuant: the rows leave as e4m3 codes and 1x128 scales; 16 lanes hold a group
@@ -274,12 +278,15 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
     moe_combine_backward_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ D, int N,
                                 const int32_t* __restrict__ pos, const float* __restrict__ w, int T, int topk,
                                 uint16_t* __restrict__ dD, uint8_t* __restrict__ q, float* __restrict__ sa, int ld_sa,
-                                float* __restrict__ dw, int M, int blocks, int pads, uint32_t* err) {
+                                float* __restrict__ dw, int tokens, int M, int blocks, int pads, uint32_t* err) {
   constexpr int kSlots = kGroup * kGroups;
   extern __shared__ __align__(16) uint8_t dyn[];  // two stages of kGroup + 1 vectors a thread
-  __shared__ long s_row[kSlots];    // first element of each slot's row, -1 if it is dropped
-  __shared__ int s_pos[kSlots];
-  __shared__ float s_w[kSlots];
+  struct Slots {
+    long row[kSlots];  // first element of each slot's row, -1 if it is dropped
+    int pos[kSlots];
+    float w[kSlots];
+  };
+  __shared__ Slots s_slots[8];  // of each of the CTA's tokens
   __shared__ float s_dot[8][kSlots];
   if (static_cast<int>(blockIdx.x) < pads) {
     __shared__ uint32_t bits[kPadBlocks * 4];
@@ -296,21 +303,25 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int own = min(lane & 15, kSlots - 1);  // the slot whose scale this lane forms
-  const int per_row = N / 8, step = blockDim.x;
-  const int steps = (per_row + step - 1) / step;
-  const uint32_t pitch = step * 16, stage = (kGroup + 1) * pitch;
+  const int step = blockDim.x / tokens;  // threads of a token
+  const int sub = threadIdx.x / step, tid = threadIdx.x - sub * step;
+  Slots& slot = s_slots[sub];
+  const int steps = (N / 8 + step - 1) / step;
+  const uint32_t pitch = blockDim.x * 16, stage = (kGroup + 1) * pitch;
   const uint32_t slot0 = fp8g::smem_u32(dyn) + threadIdx.x * 16;
-  for (long t = static_cast<long>(blockIdx.x) - pads; t < T; t += static_cast<long>(gridDim.x) - pads) {
-    if (threadIdx.x < kSlots) {
-      const int k = threadIdx.x;
-      const int p = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
-      s_pos[k] = p;
-      s_row[k] = p < 0 ? -1 : static_cast<long>(p) * N;
-      s_w[k] = k < topk && w ? __ldg(w + t * topk + k) : 1.f;
+  for (long t0 = (static_cast<long>(blockIdx.x) - pads) * tokens; t0 < T; t0 += (static_cast<long>(gridDim.x) - pads) * tokens) {
+    const long t = t0 + sub;
+    const int slots = t < T ? topk : 0;  // behind the last token there are none
+    if (tid < kSlots) {
+      const int k = tid;
+      const int p = k < slots ? checked_pos(pos, t * topk + k, M, err) : -1;
+      slot.pos[k] = p;
+      slot.row[k] = p < 0 ? -1 : static_cast<long>(p) * N;
+      slot.w[k] = k < slots && w ? __ldg(w + t * topk + k) : 1.f;
     }
     __syncthreads();
-    const uint16_t* dout_t = dout + t * N;
-    long col = 8 * threadIdx.x;   // this thread's columns: of the current vectors,
+    const uint16_t* dout_t = dout + (t < T ? t * N : 0);
+    long col = 8 * tid;   // this thread's columns: of the current vectors,
     int fetch_col = static_cast<int>(col);  // and of the next ones to fetch
     uint32_t put = slot0, get = slot0;
     // Copies the vectors of slots gi * kGroup ..; zeros for dropped slots and for
@@ -323,7 +334,7 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
         if (dw) {
 #pragma unroll
           for (int k = 0; k < kGroup; ++k) {
-            const long row = s_row[gi * kGroup + k];
+            const long row = slot.row[gi * kGroup + k];
             cp_async16_or_zero(put + (k + 1) * pitch, D + (row < 0 ? 0 : row) + c, in && row >= 0 ? 16 : 0);
           }
         }
@@ -355,11 +366,11 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
             for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(x[c]));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            amax *= fabsf(s_w[own]);
+            amax *= fabsf(slot.w[own]);
             tiny = __any_sync(0xffffffffu, amax > 0.f && amax < fp8g::quant::kTinyAmax);
             own_s = tiny ? fp8g::quant::any_scale(amax) : fp8g::quant::normal_scale(amax);
             own_y = __frcp_rn(own_s);
-            if (in && (lane & 15) < kSlots && s_pos[own] >= 0) sa[(col >> 7) * ld_sa + s_pos[own]] = own_s;
+            if (in && (lane & 15) < kSlots && slot.pos[own] >= 0) sa[(col >> 7) * ld_sa + slot.pos[own]] = own_s;
           }
         }
         // Dropped slots are worked on like the others and only not stored: with
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
             for (int k = 0; k < kGroup; ++k) {
               const float s = __shfl_sync(0xffffffffu, own_s, gi * kGroup + k, 16);
               const float y = __shfl_sync(0xffffffffu, own_y, gi * kGroup + k, 16);
-              const uint64_t nw = both(-s_w[gi * kGroup + k]);  // the quantiser takes negatives
+              const uint64_t nw = both(-slot.w[gi * kGroup + k]);  // the quantiser takes negatives
               fp8g::quant::normal_codes(Pair8{mul2(g.v[0], nw), mul2(g.v[1], nw), mul2(g.v[2], nw), mul2(g.v[3], nw)}, s, y,
                                         c[k]);
             }
@@ -385,20 +396,20 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
 #pragma unroll
             for (int k = 0; k < kGroup; ++k) {
               const float s = __shfl_sync(0xffffffffu, own_s, gi * kGroup + k, 16);
-              const uint64_t nw = both(-s_w[gi * kGroup + k]);
+              const uint64_t nw = both(-slot.w[gi * kGroup + k]);
               fp8g::quant::any_codes(Pair8{mul2(g.v[0], nw), mul2(g.v[1], nw), mul2(g.v[2], nw), mul2(g.v[3], nw)}, s, c[k]);
             }
           }
 #pragma unroll
           for (int k = 0; k < kGroup; ++k) {
-            const long row = s_row[gi * kGroup + k];
+            const long row = slot.row[gi * kGroup + k];
             if (in && row >= 0) fp8g::quant::store_code_words(q + row + col, c[k]);
           }
         } else {
 #pragma unroll
           for (int k = 0; k < kGroup; ++k) {
-            const long row = s_row[gi * kGroup + k];
-            const uint64_t ww = both(s_w[gi * kGroup + k]);
+            const long row = slot.row[gi * kGroup + k];
+            const uint64_t ww = both(slot.w[gi * kGroup + k]);
             float f[8];
             values_of(Pair8{mul2(g.v[0], ww), mul2(g.v[1], ww), mul2(g.v[2], ww), mul2(g.v[3], ww)}, f);
             if (in && row >= 0) store8<false>(dD, row + col, f);
@@ -415,20 +426,22 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
         if (lane == 0) s_dot[warp][k] = sum;
       }
     }
-    const bool dropped = threadIdx.x < kSlots && s_pos[threadIdx.x] < 0;
+    const bool dropped = tid < kSlots && slot.pos[tid] < 0;
     __syncthreads();  // also: everyone has read the slots' rows and weights
-    if (dw && static_cast<int>(threadIdx.x) < topk) {
+    if (dw && tid < slots) {
       float sum = 0.f;
-      for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) sum += s_dot[i][threadIdx.x];
-      dw[t * topk + threadIdx.x] = dropped ? 0.f : sum;
+      for (int i = 0; i < step >> 5; ++i) sum += s_dot[sub * (step >> 5) + i][tid];
+      dw[t * topk + tid] = dropped ? 0.f : sum;
     }
   }
 }
 
-// CTAs that zero padding rows: up to half as many groups of blocks as SMs, or
-// enough for their bitmaps.
+// CTAs that zero padding rows: up to a quarter as many groups of blocks as SMs, or
+// enough for their bitmaps.  Each reads all of pos (4096 x top-8, combine backward to
+// FP8 147.7 us with half as many groups as SMs, 142.7 with a quarter, 139.5 with an
+// eighth; the sort 102.8, 101 and 106.8).
 int pad_ctas(int blocks, int sms) {
-  return kPadSlices * std::max((blocks + kPadBlocks - 1) / kPadBlocks, std::min(blocks, sms / 2));
+  return kPadSlices * std::max((blocks + kPadBlocks - 1) / kPadBlocks, std::min(blocks, sms / 4));
 }
 
 // The kernel for a compile-time bound on topk: 4, 8 or 16.
@@ -444,6 +457,13 @@ int row_threads(long vecs) {
   const long steps = (vecs + 255) / 256;
   return static_cast<int>(((vecs + steps - 1) / steps + 31) / 32 * 32);
 }
+
+// Tokens of a CTA: one, or as many as give it 256 threads where the rows are
+// narrow and the tokens many: a padding CTA reads every slot's position with as many
+// threads as the others have (16384 x top-8, 512 bf16: combine backward to FP8 141 us
+// with 64 threads, 72 with 256, the sort 160 and 80; with few tokens, one each
+// spreads them over more SMs).
+int cta_tokens(int T, int threads, int sms) { return T >= 8 * sms ? 256 / threads : 1; }
 
 int check_slots(int T, int topk, int N) {
   if (T < 0 || topk < 1 || topk > kMaxTopk || N < 1 || N > 1 << 20 || static_cast<long>(T) * topk > 0x7FFFFFFFL)
@@ -489,11 +509,13 @@ extern "C" int fp8g_moe_permute(const void* x, int x_dtype, int T, int N, const 
   }
   if (R == 0) return FP8G_OK;
   const int pads = pad_ctas(blocks, sms);
-  const unsigned grid = static_cast<unsigned>(pads + std::min<long>(static_cast<long>(T) * parts, 1 << 20));
+  const int threads = row_threads(vecs), tokens = cta_tokens(T, parts == 1 ? threads : 256, sms);
+  const long items = (static_cast<long>(T) + tokens - 1) / tokens * parts;
+  const unsigned grid = static_cast<unsigned>(pads + std::min<long>(items, 1 << 20));
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    e = launch_behind(dim3(grid), row_threads(vecs), stream, kernel, static_cast<const uint4*>(x),
-                                 static_cast<int>(vecs), parts, T, topk, static_cast<const int32_t*>(pos),
+    e = launch_behind(dim3(grid), threads * tokens, stream, kernel, static_cast<const uint4*>(x),
+                                 static_cast<int>(vecs), parts, tokens, T, topk, static_cast<const int32_t*>(pos),
                                  static_cast<uint4*>(xs), blocks * 128, blocks, pads, err);
   };
   by_topk(topk, [&] { go(moe_permute_kernel<4>); }, [&] { go(moe_permute_kernel<8>); },
@@ -551,14 +573,14 @@ extern "C" int fp8g_moe_combine_backward(const uint16_t* dout, const uint16_t* D
   if (sms <= 0 || !err) return FP8G_ERR_CUDA;
   if (blocks == 0) D = dout;  // no row is read, but copies of no bytes name one
   const int pads = pad_ctas(blocks, sms);
-  const unsigned grid = static_cast<unsigned>(pads + std::min<long>(T, 32L * sms));
-  const int threads = row_threads(N / 8);
+  const int row = row_threads(N / 8), tokens = cta_tokens(T, row, sms), threads = row * tokens;
+  const unsigned grid = static_cast<unsigned>(pads + std::min<long>((static_cast<long>(T) + tokens - 1) / tokens, 32L * sms));
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
     e = allow_smem(kernel);
     if (e == cudaSuccess)
       kernel<<<grid, threads, 2 * (kGroup + 1) * threads * 16, stream>>>(dout, D, N, pos, w, T, topk, dD, q, sa, ld_sa, dw,
-                                                                        blocks * 128, blocks, pads, err);
+                                                                        tokens, blocks * 128, blocks, pads, err);
   };
   if (q)
     by_topk(topk, [&] { go(moe_combine_backward_kernel<true, 1>); }, [&] { go(moe_combine_backward_kernel<true, 2>); },

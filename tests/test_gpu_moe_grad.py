@@ -43,6 +43,7 @@ def blocks_for(T, topk, G):
 SHAPES = [  # T, topk, G, N, drop
     (1, 1, 1, 8, 0.0), (1, 8, 16, 7168, 0.0), (300, 2, 5, 384, 0.1), (129, 3, 7, 520, 0.2), (2500, 6, 256, 256, 0.0),
     (200, 12, 16, 128, 0.3), (40, 16, 200, 2112, 0.05), (9000, 4, 9, 64, 0.02), (33000, 1, 3, 8, 0.0),
+    (1187, 16, 40, 128, 0.1), (2001, 8, 32, 640, 0.05), (1185, 2, 5, 384, 0.0), (4099, 3, 6, 1024, 0.0),
 ]
 
 
