@@ -12,11 +12,14 @@
 // position outside is flagged and its slot skipped.
 //
 // Padding rows.  The rows of a used block (one that holds a routed row) that
-// no slot fills are set to zero by CTAs of their own in the same launch: each
-// takes a run of blocks, marks the rows that pos names in a bitmap in shared
-// memory, and zeroes the rest.  Reading pos (4 bytes a slot) once per such CTA
-// costs little next to the rows, and saves the workspace, the launches and
-// the atomics on memory that a map from rows to slots would need.
+// no slot fills are set to zero by CTAs of their own in the same launch, each
+// with a share of the rows of a run of blocks.  The sort learns from its layout how
+// many rows of each block are filled: until its last padding CTA has seen it, a
+// block's entry of m_indices holds that number too.  The combine's gradient
+// has only pos: its padding CTAs mark the rows that pos names in a bitmap in
+// shared memory.  Reading pos (4 bytes a slot) once per such CTA costs little
+// next to rows of some thousand columns, and saves the workspace, the launches
+// and the atomics on memory that a map from rows to slots would need.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -111,15 +114,26 @@ __device__ __forceinline__ void pad_range(int cta, int pads, int blocks, int& b0
 template <int kCap>
 __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int parts, int tokens, int T,
                                                           int topk, const int32_t* __restrict__ pos, uint4* __restrict__ xs, int M,
-                                                          int blocks, int pads, uint32_t* err) {
-  __shared__ uint32_t bits[kPadBlocks * 4];
+                                                          int32_t* m_indices, int blocks, int pads, uint32_t* err) {
   if (static_cast<int>(blockIdx.x) < pads) {
-    fp8g::grid_dependency_wait();  // pos
+    __shared__ uint8_t s_filled[kPadBlocks];
     int b0, b1, slice;
     pad_range(blockIdx.x, pads, blocks, b0, b1, slice);
-    pad_blocks(pos, static_cast<long>(T) * topk, b0, b1, slice, bits, err, [&](long row) {
-      for (int i = threadIdx.x & 31; i < vecs; i += 32) __stcs(xs + row * vecs + i, make_uint4(0u, 0u, 0u, 0u));
-    });
+    fp8g::grid_dependency_wait();  // m_indices
+    for (int b = b0 + threadIdx.x; b < b1; b += blockDim.x) {
+      int filled = 128;  // or unused
+      if (__ldcg(m_indices + b) >= 0) {
+        const int32_t entry = atomicAdd(m_indices + b, fp8g::moe::kBlockArrival);
+        filled = fp8g::moe::block_filled(entry);
+        if (fp8g::moe::block_arrivals(entry) == kPadSlices - 1) m_indices[b] = fp8g::moe::block_expert(entry);
+      }
+      s_filled[b - b0] = static_cast<uint8_t>(filled);
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    for (int b = b0; b < b1; ++b)
+      for (int row = s_filled[b - b0] + slice + kPadSlices * warp; row < 128; row += kPadSlices * nw)
+        for (int i = lane; i < vecs; i += 32) __stcs(xs + (b * 128L + row) * vecs + i, make_uint4(0u, 0u, 0u, 0u));
     return;
   }
   const int row_threads = blockDim.x / tokens, sub = threadIdx.x / row_threads, tid = threadIdx.x - sub * row_threads;
@@ -437,9 +451,9 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
 }
 
 // CTAs that zero padding rows: up to a quarter as many groups of blocks as SMs, or
-// enough for their bitmaps.  Each reads all of pos (4096 x top-8, combine backward to
-// FP8 147.7 us with half as many groups as SMs, 142.7 with a quarter, 139.5 with an
-// eighth; the sort 102.8, 101 and 106.8).
+// enough for their bitmaps.  In the combine's gradient each reads all of pos (to FP8,
+// 4096 x top-8 x 7168: 147.7 us with half as many groups as SMs, 142.7 with a quarter,
+// 139.5 with an eighth; 333 x top-4 x 4096 bf16 7.4, 7.4 and 8).
 int pad_ctas(int blocks, int sms) {
   return kPadSlices * std::max((blocks + kPadBlocks - 1) / kPadBlocks, std::min(blocks, sms / 4));
 }
@@ -461,8 +475,8 @@ int row_threads(long vecs) {
 // Tokens of a CTA: one, or as many as give it 256 threads where the rows are
 // narrow and the tokens many: a padding CTA reads every slot's position with as many
 // threads as the others have (16384 x top-8, 512 bf16: combine backward to FP8 141 us
-// with 64 threads, 72 with 256, the sort 160 and 80; with few tokens, one each
-// spreads them over more SMs).
+// with 64 threads, 72 with 256; sort of 65536 x top-4, 128 FP32: 76 and 70; with few
+// tokens, one each spreads them over more SMs).
 int cta_tokens(int T, int threads, int sms) { return T >= 8 * sms ? 256 / threads : 1; }
 
 int check_slots(int T, int topk, int N) {
@@ -516,7 +530,7 @@ extern "C" int fp8g_moe_permute(const void* x, int x_dtype, int T, int N, const 
   auto go = [&](auto kernel) {
     e = launch_behind(dim3(grid), threads * tokens, stream, kernel, static_cast<const uint4*>(x),
                                  static_cast<int>(vecs), parts, tokens, T, topk, static_cast<const int32_t*>(pos),
-                                 static_cast<uint4*>(xs), blocks * 128, blocks, pads, err);
+                                 static_cast<uint4*>(xs), blocks * 128, m_indices, blocks, pads, err);
   };
   by_topk(topk, [&] { go(moe_permute_kernel<4>); }, [&] { go(moe_permute_kernel<8>); },
           [&] { go(moe_permute_kernel<kMaxTopk>); });

@@ -118,10 +118,20 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   return r;
 }
 
+// A used block of the contiguous layout as the layout kernel leaves it for the
+// kernel that moves the rows: its expert and its filled rows (1 to 128).  That
+// kernel's padding CTAs count themselves in the bits above (kBlockArrival) and the
+// last one leaves the expert alone.
+constexpr int32_t kBlockArrival = 1 << 16;
+__device__ __forceinline__ int32_t block_entry(int g, int filled) { return g | filled << 8; }
+__device__ __forceinline__ int block_expert(int32_t entry) { return entry & 0xFF; }
+__device__ __forceinline__ int block_filled(int32_t entry) { return entry >> 8 & 0xFF; }
+__device__ __forceinline__ int block_arrivals(int32_t entry) { return entry >> 16; }
+
 // kMasked: pos[r] = g * Mmax + rank, -1 at and behind Mmax; counts[g] =
 // min(rows of g, Mmax).  Otherwise the contiguous layout: pos[r] = first row
-// of g's segment + rank, segments padded to 128 rows; counts = m_indices
-// [blocks].  Launched as one cluster of 1 to 8 CTAs.
+// of g's segment + rank, segments padded to 128 rows; counts [blocks] = a
+// block_entry, -1 for an unused block.  Launched as one cluster of 1 to 8 CTAs.
 template <bool kMasked>
 __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_t* __restrict__ expert, int R, int G,
                                                                     int Mmax, int32_t* __restrict__ pos,
@@ -130,7 +140,8 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_
   __shared__ int32_t s_w[kLayoutWarps][kMaxExperts];  // per warp: slots of each expert, then the warp's next rank
   __shared__ int32_t s_total[kMaxExperts];            // this CTA's slots of each expert (read by the cluster)
   __shared__ int32_t s_first[kMaxExperts];            // first row that this CTA hands out for each expert
-  __shared__ int32_t s_end[kMaxExperts];              // contiguous: end of each segment in blocks
+  __shared__ int32_t s_end[kMaxExperts];              // contiguous: end of each segment in blocks,
+  __shared__ int32_t s_rows[kMaxExperts];             // and its rows
   __shared__ int32_t s_warp[kMaxExperts / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
@@ -214,6 +225,7 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_
     if (tid < kMaxExperts) {
       for (int i = 0; i < w; ++i) incl += s_warp[i];
       s_end[tid] = incl;
+      s_rows[tid] = total;
       s_first[tid] = (incl - nblk) * 128 + before;
     }
     __syncthreads();
@@ -225,7 +237,8 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const int32_
         if (s_end[mid] > b) hi = mid;
         else lo = mid + 1;
       }
-      counts[b] = lo < G ? lo : -1;
+      // only a segment's last block is not full
+      counts[b] = lo < G ? block_entry(lo, b + 1 < s_end[lo] ? 128 : (s_rows[lo] - 1) % 128 + 1) : -1;
     }
   }
   for (long i0 = 0; i0 < steps; i0 += kAhead) {
