@@ -505,6 +505,7 @@ struct Plan {
   int threads;
   int smem;
   long clusters;
+  long limit;  // clusters never exceed it, and it does not fall as the rows grow
 };
 
 constexpr int kSms = 148;
@@ -532,6 +533,7 @@ Plan plan_of(int rows, int H, int esz, int tensors, int unit, int vecs, int sm_t
   // same number of rows or one less
   const long most = std::max(1L, std::min(static_cast<long>(kSms) * per_sm / p.ctas, most_clusters));
   const long rounds = std::max(1L, (rows + most - 1) / most);
+  p.limit = std::max(1L, std::min(static_cast<long>(rows), most));
   p.clusters = std::max(1L, (rows + rounds - 1) / rounds);
   return p;
 }
@@ -631,8 +633,10 @@ extern "C" int fp8g_norm_residual(const void* y, const void* h, int dtype, int r
 
 extern "C" size_t fp8g_norm_residual_backward_workspace_bytes(int rows, int H) {
   if (rows < 0 || H <= 0 || H > kMaxH || H % 8 != 0) return 0;
-  // the larger of the two types' plans
-  const long n = std::max(backward_plan(rows, H, FP8G_IN_BF16).clusters, backward_plan(rows, H, FP8G_IN_F32).clusters);
+  // The larger of the two types' limits, not the plan's clusters: those even out the
+  // rows of a cluster, so that 148 rows of 7168 have more of them (148) than 8192 (147),
+  // and a workspace made for the larger batch would not do for the smaller one.
+  const long n = std::max(backward_plan(rows, H, FP8G_IN_BF16).limit, backward_plan(rows, H, FP8G_IN_F32).limit);
   const long sums = n > kOneLaunch ? (n + kPartsPerSum - 1) / kPartsPerSum : 0;
   return static_cast<size_t>(2 * (n + sums) * H) * sizeof(float);
 }

@@ -590,7 +590,8 @@ def norm_residual_backward(dz, dh_out, h_out, y, post_weight=None, gate=None, sc
     parameters' shapes, None where the parameter is None.  h_out and y are the
     forward pass's.  `out` may pass the five tensors to reuse them (dh may be
     dh_out), `workspace` float32 scratch of at least
-    fp8g_norm_residual_backward_workspace_bytes(rows, H) bytes."""
+    fp8g_norm_residual_backward_workspace_bytes(rows, H) bytes (of the largest
+    batch, to keep one for all)."""
     dev = _rows(y, "y")
     rows, H = y.shape
     _operand(h_out, y.dtype, (rows, H), dev, "h_out")

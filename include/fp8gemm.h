@@ -406,8 +406,9 @@ int fp8g_norm_residual(const void *y, const void *h, int dtype, int rows, int H,
  *   NULL if it is not wanted (dpost_w needs post_w, dgate needs gate).
  *   workspace: >= fp8g_norm_residual_backward_workspace_bytes(rows, H) bytes,
  *   16-byte aligned, overwritten; needed for dpre_w, dpost_w and a channel
- *   gate's dgate, otherwise it may be NULL.  Calls that may overlap on the GPU
- *   need a workspace each.
+ *   gate's dgate, otherwise it may be NULL.  The size does not fall as rows
+ *   grow: one for the largest batch serves the smaller ones.  Calls that may
+ *   overlap on the GPU need a workspace each.
  * dh may be dh_out's buffer.  With rows == 0 the weights' gradients are set
  * to zero.  Sums over rows run in a fixed order: the same call gives the same
  * bits.  Errors of both: FP8G_ERR_INVALID_ARG, FP8G_ERR_MISALIGNED (rows and

@@ -377,3 +377,21 @@ def test_parameters_beside_other_rows_stay_untouched(g):
     assert bool((big[0] == -7).all()) and bool((big[-1] == -7).all())
     assert bool((q[0] == 0x5A).all()) and bool((q[-1] == 0x5A).all()) and bool((sa[:, rows:] == -3).all())
     assert bool((sa[:, :rows] > 0).all())
+
+
+@pytest.mark.parametrize("H,most", [(1024, 8192), (4096, 1000), (12416, 700)])
+def test_one_workspace_for_the_largest_batch(g, H, most):
+    """The workspace of the largest batch serves smaller ones, whatever was left
+    in it, and nothing is written behind it."""
+    need = g.lib.fp8g_norm_residual_backward_workspace_bytes(most, H) // 4
+    kept = torch.full((need + 64,), float("nan"), device="cuda")
+    x, gen = inputs(most, most, H, torch.bfloat16, True, "channel", True, True)
+    dz = torch.randn(most, H, generator=gen).to(torch.bfloat16).cuda()
+    y, h = dev(x["y"]), dev(x["h"])
+    kw = dict(post_weight=dev(x["post_w"]), gate=dev(x["gate"]), scale=0.5, pre_weight=dev(x["pre_w"]), eps=EPS)
+    for rows in (most, most // 2 + 1, 592, 148, 1):
+        if rows <= most:
+            want = g.norm_residual_backward(dz[:rows], None, h[:rows], y[:rows], **kw)
+            got = g.norm_residual_backward(dz[:rows], None, h[:rows], y[:rows], workspace=kept[:need], **kw)
+            assert all(torch.equal(a, b) for a, b in zip(want, got)), rows
+    assert bool(torch.isnan(kept[need:]).all())

@@ -131,6 +131,16 @@ def test_workspace_sizes(gemm):
     assert f(1 << 30, 16384) < 1 << 28      # bounded by the GPU, not by the rows
 
 
+@pytest.mark.parametrize("H", [8, 128, 520, 1024, 2048, 2112, 4096, 7168, 8200, 12416, 16384])
+def test_a_workspace_for_the_largest_batch_serves_every_smaller_one(gemm, H):
+    """A caller keeps one workspace for its largest batch: the size never falls
+    as the rows grow, past the row counts where the rows of a CTA go up by one
+    (multiples of 148 and of what a smaller grid has) too."""
+    f = gemm.lib.fp8g_norm_residual_backward_workspace_bytes
+    sizes = [f(r, H) for r in range(0, 12000)] + [f(r, H) for r in (1 << 14, 148 * 997, 1 << 20, 1 << 30, 2 ** 31 - 1)]
+    assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU error path")
 @pytest.mark.parametrize("name,good", [("fp8g_moe_dispatch_masked", MASKED), ("fp8g_moe_permute", PERMUTE),
                                        ("fp8g_moe_permute_backward", PERMUTE_BWD),
