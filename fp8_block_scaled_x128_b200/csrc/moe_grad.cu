@@ -45,10 +45,9 @@ constexpr int kPadSlices = 8;
 // layout kernel, and one launch on the host).
 constexpr int kDirectSlots = 4096;
 
-// pos[r] if it names a row of the layout, -1 if the slot is dropped; anything
-// else is flagged and treated as dropped.
-__device__ __forceinline__ int checked_pos(const int32_t* pos, long r, int M, uint32_t* err) {
-  const int p = __ldg(pos + r);
+// A slot's position if it names a row of the layout, -1 if the slot is dropped;
+// anything else is flagged and treated as dropped.
+__device__ __forceinline__ int checked_pos(int p, int M, uint32_t* err) {
   if (p >= -1 && p < M) return p;
   atomicOr(err, FP8G_DEVERR_BAD_POS);
   return -1;
@@ -108,12 +107,14 @@ __device__ __forceinline__ void pad_range(int cta, int pads, int blocks, int& b0
 // CTAs [0, pads) zero padding rows; the others take a part of a token's row
 // each, one 16-byte vector a thread, whatever the type: short CTAs leave little
 // work behind when the last ones run (with a CTA per token, 3.5 waves of 8 CTAs
-// an SM, the last wave ran half empty).  4096 tokens x top-8 over 64 experts, 7168
+// an SM, the last wave ran half empty).  pos and m_indices are read by coherent loads
+// (and pos is not __restrict__): the layout kernel still writes them when this one
+// starts.  4096 tokens x top-8 over 64 experts, 7168
 // bf16: 101 us with the layout kernel (of which some 7 us are not hidden), 588 MB
 // with the padding rows: 0.89 of the measured copy bandwidth.
 template <int kCap>
 __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int parts, int tokens, int T,
-                                                          int topk, const int32_t* __restrict__ pos, uint4* __restrict__ xs, int M,
+                                                          int topk, const int32_t* pos, uint4* __restrict__ xs, int M,
                                                           int32_t* m_indices, int blocks, int pads, uint32_t* err) {
   if (static_cast<int>(blockIdx.x) < pads) {
     __shared__ uint8_t s_filled[kPadBlocks];
@@ -152,10 +153,13 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restric
   fp8g::grid_dependency_wait();                                     // pos does
   while (i < items) {
     const long j = at - t * vecs;
+    int p[kCap];
+#pragma unroll
+    for (int k = 0; k < kCap; ++k) p[k] = k < topk && t < T ? pos[t * topk + k] : -1;
 #pragma unroll
     for (int k = 0; k < kCap; ++k) {
-      const int p = k < topk && t < T ? checked_pos(pos, t * topk + k, M, err) : -1;
-      if (p >= 0 && at >= 0) __stcs(xs + static_cast<long>(p) * vecs + j, v);
+      const int row = checked_pos(p[k], M, err);
+      if (row >= 0 && at >= 0) __stcs(xs + static_cast<long>(row) * vecs + j, v);
     }
     i += stride;
     if (i < items) {
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* _
   for (long t = blockIdx.x; t < T; t += gridDim.x) {
     int p[kCap];
 #pragma unroll
-    for (int k = 0; k < kCap; ++k) p[k] = k < topk ? checked_pos(pos, t * topk + k, M, err) : -1;
+    for (int k = 0; k < kCap; ++k) p[k] = k < topk ? checked_pos(__ldg(pos + t * topk + k), M, err) : -1;
     for (int j = threadIdx.x; j < N / 8; j += blockDim.x) {
       Raw8<kF32> v[kCap];
 #pragma unroll
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
     const int slots = t < T ? topk : 0;  // behind the last token there are none
     if (tid < kSlots) {
       const int k = tid;
-      const int p = k < slots ? checked_pos(pos, t * topk + k, M, err) : -1;
+      const int p = k < slots ? checked_pos(__ldg(pos + t * topk + k), M, err) : -1;
       slot.pos[k] = p;
       slot.row[k] = p < 0 ? -1 : static_cast<long>(p) * N;
       slot.w[k] = k < slots && w ? __ldg(w + t * topk + k) : 1.f;

@@ -450,11 +450,12 @@ __global__ void __maxnreg__(backward_regs(kF32, V))
 // at a time, then the warps' sums in warp order (8192 x 7168, 148 partial rows:
 // latency of one or two rounds of loads).  Many partial rows (narrow
 // rows have many CTAs) are summed in two launches: to out[2][gridDim.y][H]
-// first, then to the gradients (kLast).
+// first, then to the gradients (kLast).  part is read by coherent loads: this kernel
+// starts while the one that writes it still runs.
 constexpr int kSumWarps = 32;
 
 template <bool kLast>
-__global__ void __launch_bounds__(32 * kSumWarps, 2) norm_param_grad_kernel(const float* __restrict__ part, int P, int H, int per,
+__global__ void __launch_bounds__(32 * kSumWarps, 2) norm_param_grad_kernel(const float* part, int P, int H, int per,
                                                               float* __restrict__ out, Params prm, float* dpre,
                                                               float* dpost, float* dgate) {
   __shared__ float s[2][kSumWarps][32];
@@ -469,8 +470,8 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) norm_param_grad_kernel(cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int q = p + i * kSumWarps;
-        x[i] = q < p1 ? part[static_cast<long>(q) * H + col] : 0.f;
-        y[i] = q < p1 ? part[(static_cast<long>(P) + q) * H + col] : 0.f;
+        x[i] = q < p1 ? __ldcg(part + static_cast<long>(q) * H + col) : 0.f;
+        y[i] = q < p1 ? __ldcg(part + (static_cast<long>(P) + q) * H + col) : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) a += x[i], b += y[i];
