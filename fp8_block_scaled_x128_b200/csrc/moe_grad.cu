@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(256, kGroups == 4 ? 2 : kQuant || kGroups == 1
             for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             amax *= fabsf(slot.w[own]);
             tiny = __any_sync(0xffffffffu, amax > 0.f && amax < fp8g::quant::kTinyAmax);
-            own_s = tiny ? fp8g::quant::any_scale(amax) : fp8g::quant::normal_scale(amax);
+            own_s = tiny ? fp8g::quant::scale_of(amax) : fp8g::quant::normal_scale(amax);
             own_y = __frcp_rn(own_s);
             if (in && (lane & 15) < kSlots && slot.pos[own] >= 0) sa[(col >> 7) * ld_sa + slot.pos[own]] = own_s;
           }

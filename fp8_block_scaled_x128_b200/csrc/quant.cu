@@ -6,7 +6,7 @@
 // DeepGEMM 오픈소스 공개", topic body, first bullet): one FP32 scale per 1x128
 // row group of the activations A and per 128x128 block of the weights B.
 //
-//   scale = amax / 448 (FP32; 1 for an all-zero group),
+//   scale = amax / 448 (FP32; 1 where that rounds to zero),
 //   code  = e4m3_rne_satfinite(x / scale)   (one IEEE FP32 division)
 //
 // Both kernels are HBM-bound streams: each input element is read once (2 or
@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(256) quantize_128x128_kernel(const void* __res
   amax = warp_max[0];
 #pragma unroll
   for (int w = 1; w < 8; ++w) amax = fmaxf(amax, warp_max[w]);
-  const float s = scale_of(amax);
+  // 7168 x 16384 bf16: 71.0 to 72.5 us with a branch around the division, 72.8 without
+  const float s = amax > 0.f ? scale_of(amax) : 1.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 16 * i;

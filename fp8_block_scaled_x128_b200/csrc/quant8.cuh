@@ -2,7 +2,7 @@
 // magnitude is known: the codes and scale of quant_impl.cuh's definition, bit
 // for bit, at fewer instructions.
 //
-//   scale = fl(amax / 448) (1 for an all-zero group), code = e4m3(fl(x / scale))
+//   scale = fl(amax / 448) (1 where that is zero), code = e4m3(fl(x / scale))
 //
 // quant_impl.cuh divides amax by 448 in IEEE arithmetic and multiplies every
 // value by a power of two that is 1 for all but tiny groups.  Here both
@@ -44,14 +44,7 @@ __device__ __forceinline__ void normal_codes(const rows::Pair8& neg, float s, fl
   for (int i = 0; i < 2; ++i) c[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | (e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16);
 }
 
-// The general path, for groups of any magnitude.  amax / 448 rounds to zero below
-// 3.2e-43; such a group, whose quotients the definition leaves without a value
-// (x / 0), is an all-zero group: scale 1, codes of zeros.
-__device__ __forceinline__ float any_scale(float amax) {
-  const float s = scale_of(amax);
-  return s > 0.f ? s : 1.f;
-}
-
+// The general path, for groups of any magnitude: quant_impl.cuh's scale_of, and its codes.
 __device__ __forceinline__ void any_codes(const rows::Pair8& neg, float s, uint32_t (&c)[2]) {
   float v[8];
   rows::values_of(neg, v);
@@ -64,7 +57,7 @@ __device__ __forceinline__ void any_codes(const rows::Pair8& neg, float s, uint3
 // given the values' negatives.  All 32 lanes call it.
 __device__ __forceinline__ void quantize8(const rows::Pair8& neg, float amax, float& s, uint32_t (&c)[2]) {
   if (__any_sync(0xffffffffu, amax > 0.f && amax < kTinyAmax)) {
-    s = any_scale(amax);
+    s = scale_of(amax);
     any_codes(neg, s, c);
   } else {
     s = normal_scale(amax);

@@ -2,7 +2,8 @@
 // groups and 128x128 blocks, shared by the quantiser kernels (quant.cu) and
 // the expert dispatch (moe.cu).
 //
-//   scale = amax / 448 (FP32; 1 for an all-zero group),
+//   scale = amax / 448 (FP32; 1 where that rounds to zero: an all-zero group, or
+//           amax <= 224 * 2^-149, whose codes are zeros too),
 //   code  = e4m3_rne_satfinite(x / scale)   (one IEEE FP32 division)
 //
 // The division.  A full IEEE division per element would make the kernels
@@ -24,7 +25,10 @@ namespace quant {
 constexpr float kE4M3Max = 448.0f;
 constexpr int kUnits = 8;  // 16-byte loads per lane in flight per warp
 
-__device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? __fdiv_rn(amax, kE4M3Max) : 1.f; }
+__device__ __forceinline__ float scale_of(float amax) {
+  const float s = __fdiv_rn(amax, kE4M3Max);
+  return s > 0.f ? s : 1.f;
+}
 
 // Two floats -> two e4m3 codes (round to nearest even, saturating at +-448),
 // lo in the low byte.

@@ -185,7 +185,9 @@ int fp8g_sa_to_mn_major(const float *src, float *dst, int G, int rows, int KB, i
  * DeepGEMM 오픈소스 공개", topic body, first bullet: fine-grained scaling).
  * For every group G of input values:
  *     scale = amax(|G|) / 448   in FP32 (448 = the largest finite e4m3 value;
- *                               scale = 1 when every value of G is zero)
+ *                               scale = 1 where that is zero: every value of
+ *                               G is zero, or amax <= 224 * 2^-149 = 3.1e-43;
+ *                               the codes are zeros then)
  *     code  = e4m3 of the FP32 quotient x / scale, rounded to nearest even,
  *             saturating at +-448 (one IEEE FP32 division per element).
  * The outputs are the GEMM calls' inputs, in their layouts.  Inputs must be
@@ -286,8 +288,7 @@ int fp8g_moe_combine(const uint16_t *D, int N, const int32_t *pos, const float *
  * fp8g_moe_dispatch, in front of m_grouped_fp8_gemm_nt_masked (GeekNews,
  * "마스킹(masked) 레이아웃의 그룹화 GEMM").  Expert g's slots, in their order r,
  * take rows 0, 1, ... of group g; token t is quantised per 1x128 group as by
- * fp8g_quantize_1x128.  (Here and in the calls below a group so small that its
- * scale would round to zero, amax < 3.2e-43, counts as an all-zero group.)
+ * fp8g_quantize_1x128.
  *   x [T][K] (bf16 patterns or FP32, x_dtype), K % 128 == 0, K <= 65536;
  *   x finite; expert [T*topk] int32, -1 = dropped; 1 <= topk <= 16;
  *   1 <= G <= 256;

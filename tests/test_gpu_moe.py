@@ -140,3 +140,22 @@ def test_dispatch_gemm_combine_end_to_end(g):
     lim = 8e-3 * mag + 1e-3 * rms * wsum + 4e-3 * np.abs(ref)
     assert np.all(err <= lim), f"{int(np.sum(err > lim))} elements out of tolerance, worst {np.max(err - lim)}"
     assert g.device_error() == 0
+
+
+def test_tokens_of_the_smallest_floats_in_both_dispatches(g):
+    """Groups whose scale would round to zero: both dispatches give the
+    quantiser's codes and scales of each token, none of them NaN."""
+    T, K, topk, G = 9, 256, 2, 3
+    rng = np.random.default_rng(3)
+    x = (rng.integers(-1, 2, (T, K)) * np.arange(1, T + 1)[:, None] * 40 * 2.0 ** -149).astype(np.float32)
+    x[:, 128:] = rng.standard_normal((T, 128))
+    e = routing(4, T, topk, G)
+    xd, ed = torch.from_numpy(x).cuda(), torch.from_numpy(e).cuda()
+    q, sq = (host(t) for t in g.quantize_1x128(xd))
+    A, sa, pos, _ = (host(t) for t in g.moe_dispatch(xd, ed, topk, G))
+    Am, sm, posm, _ = (host(t) for t in g.moe_dispatch_masked(xd, ed, topk, G, 32))
+    tok = np.arange(T * topk) // topk
+    assert np.array_equal(A[pos], q[tok]) and np.array_equal(Am.reshape(G * 32, K)[posm], q[tok])
+    assert np.array_equal(sa[:, pos], sq[:, tok])
+    assert np.array_equal(sm.transpose(1, 0, 2).reshape(K // 128, G * 32)[:, posm], sq[:, tok])
+    assert not (q & 0x7F == 0x7F).any() and (sq[0, :5] == 1).all() and (sq[0, 5:T] > 0).all()

@@ -121,3 +121,41 @@ def test_quantized_operands_feed_the_gemm(g):
     ex, _ = oracle.gemm_nt(eqa, esa, esa.shape[1], eqb, esb, M, N, K)
     torch.cuda.synchronize()
     assert_close(D.view(torch.int16).cpu().numpy().view(np.uint16), ex, "quantise -> GEMM")
+
+
+def with_gone_groups(x, q, scale):
+    """The oracle's codes and scales of groups x [n, ...] (q alike, scale [n]), with
+    the groups whose scale rounds to zero, where the oracle divides by zero, as
+    all-zero ones: scale 1, zero codes with the values' signs."""
+    gone = scale == 0
+    units = np.abs(x).reshape(len(x), -1).max(1).astype(np.float64) / 2.0 ** -149
+    assert np.array_equal(gone, (units > 0) & (units <= 224))   # 224 / 448 is a tie, and rounds to zero
+    zero = (np.signbit(x) * 0x80).astype(np.uint8)
+    return np.where(gone.reshape(-1, *[1] * (x.ndim - 1)), zero, q), np.where(gone, np.float32(1), scale)
+
+
+def test_groups_of_the_smallest_floats(g):
+    """amax from the smallest float up, on both sides of the point where amax /
+    448 rounds to zero: no NaN codes."""
+    units = [0, 1, 2, 100, 223, 224, 225, 335, 336, 337, 448, 671, 672, 673, 1000, 2 ** 20]
+    x = np.zeros((len(units), 256), np.float32)
+    for r, u in enumerate(units):
+        part = np.array([u * k // 127 for k in range(128)]) * 2.0 ** -149
+        x[r, :128] = np.where(np.arange(128) % 3 == 1, -part, part)
+        x[r, 128:] = 3.0 - np.arange(128) / 32            # a neighbouring group of ordinary size
+    q, sa = (host(t) for t in g.quantize_1x128(to_dev(x, "f32")))
+    eq, esa = oracle.quantize_1x128(x, ld_sa=sa.shape[1])
+    for kb in (0, 1):
+        cols = slice(128 * kb, 128 * kb + 128)
+        want, scale = with_gone_groups(x[:, cols], eq[:, cols], esa[kb, :len(units)])
+        assert np.array_equal(q[:, cols], want) and np.array_equal(sa[kb, :len(units)], scale)
+    assert not (q & 0x7F == 0x7F).any()
+    for u in units:
+        w = np.zeros((200, 256), np.float32)
+        w[3, 5], w[130, 7], w[150, 200] = u * 2.0 ** -149, -u * 2.0 ** -149, 1.0
+        q, sb = (host(t) for t in g.quantize_128x128(to_dev(w, "f32")))
+        eq, esb = oracle.quantize_128x128(w)
+        for nb, kb in np.ndindex(2, 2):
+            at = np.s_[128 * nb:128 * nb + 128, 128 * kb:128 * kb + 128]
+            want, scale = with_gone_groups(w[at][None], eq[at][None], esb[nb, kb][None])
+            assert np.array_equal(q[at], want[0]) and sb[nb, kb] == scale[0]
