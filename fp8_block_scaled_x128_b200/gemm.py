@@ -8,6 +8,7 @@ the shared library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 
 import torch
@@ -357,6 +358,11 @@ def _operand(t, dt, shape, index, name):
     return t
 
 
+def _slots(t, R, index, name):
+    """t, if it is a contiguous int32 CUDA tensor of R routed slots, flat or [T, topk]."""
+    return _operand(t, torch.int32, t.shape if math.prod(t.shape) == R else (R,), index, name)
+
+
 def _rows(t, name):
     """The device index of t, if it is a contiguous 2-D CUDA tensor of activations."""
     if t.dtype not in _IN_DTYPE or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
@@ -389,16 +395,16 @@ def _addr(t):
 
 def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
     """Expert dispatch before the masked GEMM: x [T, K] (bfloat16 or float32),
-    expert [T*topk] int32 (-1 = dropped) -> (A [G, Mmax, K] uint8, sa [G, K/128,
-    ld_sa] float32, pos [T*topk] int32, masked_m [G] int32).  pos is the slot's
-    row of D seen as [G*Mmax, N], for moe_combine; slots past an expert's Mmax
-    rows are dropped and flagged (DEVERR_MASKED_OVER).  Rows behind masked_m
-    are not written.  `out` may pass those four tensors to reuse them."""
+    expert [T*topk] or [T, topk] int32 (-1 = dropped) -> (A [G, Mmax, K] uint8,
+    sa [G, K/128, ld_sa] float32, pos [T*topk] int32, masked_m [G] int32).  pos
+    is the slot's row of D seen as [G*Mmax, N], for moe_combine; slots past an
+    expert's Mmax rows are dropped and flagged (DEVERR_MASKED_OVER).  Rows behind
+    masked_m are not written.  `out` may pass those four tensors to reuse them."""
     dev = _rows(x, "x")
     T, K = x.shape
     topk, G, Mmax = int(topk), int(G), int(Mmax)
     R = T * topk
-    _operand(expert, torch.int32, (R,), dev, "expert")
+    _slots(expert, R, dev, "expert")
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
@@ -423,15 +429,16 @@ def moe_dispatch_masked(x, expert, topk, G, Mmax, out=None, stream=None):
 
 def moe_permute(x, expert, topk, G, blocks=None, out=None, stream=None):
     """Expert sort without quantisation, in moe_dispatch's contiguous layout: x
-    [T, N] (bfloat16 or float32), expert [T*topk] int32 (-1 = dropped) -> (xs
-    [blocks*128, N] of x's type, pos [T*topk] int32, m_indices [blocks] int32).
+    [T, N] (bfloat16 or float32), expert [T*topk] or [T, topk] int32 (-1 =
+    dropped) -> (xs [blocks*128, N] of x's type, pos [T*topk] int32, m_indices
+    [blocks] int32).
     Padding rows of a segment are zero; unused blocks are not written.  `out`
     may pass those three tensors to reuse them."""
     dev = _rows(x, "x")
     T, N = x.shape
     topk, G = int(topk), int(G)
     R = T * topk
-    _operand(expert, torch.int32, (R,), dev, "expert")
+    _slots(expert, R, dev, "expert")
     nb = moe_blocks(T, topk, G) if blocks is None else int(blocks)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -452,12 +459,13 @@ def moe_permute(x, expert, topk, G, blocks=None, out=None, stream=None):
 def moe_permute_backward(dxs, pos, T, topk, out=None, stream=None):
     """Gradient of moe_permute (and of moe_dispatch, its quantisation taken as
     the identity): dx [T, N] = sum over a token's slots of dxs[pos] (FP32 in
-    slot order, rounded once).  dxs [blocks*128, N] bfloat16 or float32."""
+    slot order, rounded once).  dxs [blocks*128, N] bfloat16 or float32; pos
+    [T*topk] or [T, topk]."""
     dev = _rows(dxs, "dxs")
     M, N = dxs.shape
     T, topk = int(T), int(topk)
     _layout_rows(M, "dxs")
-    _operand(pos, torch.int32, (T * topk,), dev, "pos")
+    _slots(pos, T * topk, dev, "pos")
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
@@ -478,8 +486,8 @@ def _layout_rows(M, name):
 
 
 def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, stream=None):
-    """Gradient of moe_combine: dout [T, N], D [blocks*128, N] bfloat16, w
-    [T*topk] float32 or None -> (dD, dw), dD [blocks*128, N] bfloat16 with
+    """Gradient of moe_combine: dout [T, N], D [blocks*128, N] bfloat16, pos
+    [T*topk] or [T, topk], w [T*topk] float32 or None -> (dD, dw), dD [blocks*128, N] bfloat16 with
     dD[pos] = w * dout, dw [T*topk] float32 = <dout, D[pos]> (0 for dropped
     slots; None if w is None).  quantize=True gives (q, sa, dw) instead: e4m3
     codes and [N/128, ld_sa] scales, the A side of the grouped GEMM that
@@ -490,7 +498,7 @@ def moe_combine_backward(dout, D, pos, w, T, topk, quantize=False, out=None, str
     M, N = D.shape
     _layout_rows(M, "D")
     dev = D.get_device()
-    _operand(dout, torch.bfloat16, (T, N), dev, "dout"), _operand(pos, torch.int32, (T * topk,), dev, "pos")
+    _operand(dout, torch.bfloat16, (T, N), dev, "dout"), _slots(pos, T * topk, dev, "pos")
     if w is not None:
         _operand(w, torch.float32, (T * topk,), dev, "w")
     ctx = _elsewhere(dev, stream)

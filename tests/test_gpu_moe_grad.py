@@ -496,3 +496,22 @@ def test_calls_on_other_streams_and_in_graphs(g):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want[i], got))
     assert nb * 128 >= T * topk and g.device_error() == 0
+
+
+def test_slots_in_the_shape_of_the_router(g):
+    """Experts and positions as [T, topk] tensors give what flat ones give."""
+    T, topk, G, N = 70, 3, 5, 256
+    x, e = cuda(tokens(6, T, N), torch.bfloat16), cuda(routing(7, T, topk, G, 0.1))
+    xs, pos, mi = g.moe_permute(x, e, topk, G)
+    xs2, pos2, mi2 = g.moe_permute(x, e.view(T, topk), topk, G)
+    used = int((mi >= 0).sum()) * 128
+    assert torch.equal(xs[:used], xs2[:used]) and torch.equal(pos, pos2) and torch.equal(mi, mi2)
+    assert torch.equal(g.moe_permute_backward(xs, pos, T, topk), g.moe_permute_backward(xs, pos.view(T, topk), T, topk))
+    w = torch.rand(T * topk, device="cuda")
+    for a, b in zip(g.moe_combine_backward(x, xs, pos, w, T, topk), g.moe_combine_backward(x, xs, pos.view(T, topk), w, T, topk)):
+        assert torch.equal(a[:used], b[:used])
+    a, b = (g.moe_dispatch_masked(x, s, topk, G, 128) for s in (e, e.view(T, topk)))
+    assert torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
+    A, B = a[0].view(-1, N), b[0].view(-1, N)
+    live = a[2][a[2] >= 0].long()
+    assert torch.equal(A[live], B[live]) and g.device_error() == 0

@@ -209,3 +209,29 @@ def test_binding_refuses_operands_on_two_devices(gemm):
         gemm.norm_residual(x, fake((4, 256), index=1))
     with pytest.raises(ValueError, match="one device"):
         gemm.norm_residual_backward(x, None, x, fake((4, 256), index=2))
+
+
+class OtherStream:
+    """On another device than the operands: refused behind the operands' checks."""
+    device = torch.device("cuda", 1)
+
+
+def test_binding_takes_slots_of_any_shape(gemm):
+    """A router's [T, topk] experts, and positions kept in that shape, as the
+    quantised dispatch and the combine take them."""
+    x, e = fake((4, 256)), fake((4, 2), I32)
+    for call_it in (lambda: gemm.moe_permute(x, e, 2, 4, stream=OtherStream),
+                    lambda: gemm.moe_dispatch_masked(x, e, 2, 4, 64, stream=OtherStream),
+                    lambda: gemm.moe_permute_backward(fake((128, 64)), e, 4, 2, stream=OtherStream),
+                    lambda: gemm.moe_combine_backward(x, fake((128, 256)), e, None, 4, 2, stream=OtherStream)):
+        with pytest.raises(ValueError, match="stream is on"):
+            call_it()
+    for bad in (fake((4, 3), I32), fake((4, 2), torch.int64), fake((2, 4, 2), I32)):
+        with pytest.raises(TypeError, match="expert"):
+            gemm.moe_permute(x, bad, 2, 4)
+        with pytest.raises(TypeError, match="expert"):
+            gemm.moe_dispatch_masked(x, bad, 2, 4, 64)
+        with pytest.raises(TypeError, match="pos"):
+            gemm.moe_permute_backward(fake((128, 64)), bad, 4, 2)
+        with pytest.raises(TypeError, match="pos"):
+            gemm.moe_combine_backward(x, fake((128, 256)), bad, None, 4, 2)
