@@ -395,3 +395,37 @@ def test_one_workspace_for_the_largest_batch(g, H, most):
             got = g.norm_residual_backward(dz[:rows], None, h[:rows], y[:rows], workspace=kept[:need], **kw)
             assert all(torch.equal(a, b) for a, b in zip(want, got)), rows
     assert bool(torch.isnan(kept[need:]).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,H,post,gate", [(3001, 520, True, "channel"), (5003, 72, True, "channel"),
+                                              (5003, 72, False, "channel"), (2777, 200, True, "token")])
+def test_parameter_sums_of_many_rows(g, rows, H, post, gate, dtype):
+    """More than 256 partial rows, added in two launches, with a last group of
+    columns that is not full.  The bound counts the additions on one term's way: at
+    most rows / 257 + 1 in its cluster, 4 in a warp and 32 over the warps in the first
+    launch, 1 and 32 in the second, and 30 U for the term itself.  A row left out
+    or taken twice would show: most of its terms are above the bound."""
+    assert g.lib.fp8g_norm_residual_backward_workspace_bytes(rows, H) > 2 * 257 * H * 4
+    x, gen = inputs(rows * H, rows, H, dtype, post, gate, True, True)
+    dz, dho = (torch.randn(rows, H, generator=gen).to(dtype) for _ in range(2))
+    got = g.norm_residual_backward(dev(dz), dev(dho), dev(x["h"]), dev(x["y"]), post_weight=dev(x["post_w"]),
+                                   gate=dev(x["gate"]), scale=x["scale"], pre_weight=dev(x["pre_w"]), eps=EPS)
+    y, hp, post_w, gt, s, pre_w, eps = args64(x)
+    r = ref.backward(dbl(dz), dbl(dho), hp, y, post_w, gt, s, pre_w, eps)
+    u = y * ref.rms_factor(y, eps) if post else y
+    terms = {"dpre": (dbl(dz) * hp * ref.rms_factor(hp, eps), 0.0)}
+    if post:
+        terms["dpost"] = (s * gt * r["dh"] * u, (s * gt * u).abs() * r["e_dh"])
+    if gate == "channel":
+        w2 = post_w if post else torch.ones(1, dtype=torch.float64)
+        terms["dgate"] = (s * w2 * r["dh"] * u, (s * w2 * u).abs() * r["e_dh"])
+    for t, name in zip(got[2:], ("dpre", "dpost", "dgate")):
+        if name not in terms:
+            continue
+        each, err = terms[name]
+        bound = (rows // 257 + 70 + 30) * ref.U * each.abs().sum(0) + (err.sum(0) if torch.is_tensor(err) else err)
+        shown = (each.abs() > 2 * bound).double().mean(1) > 0.5
+        assert bool(shown.all()) if gate == "channel" else float(shown.double().mean()) > 0.9   # a token's gate may be near 0
+        within(t, each.sum(0), rounded(each.sum(0), bound, torch.float32), name)
+    assert g.device_error() == 0
