@@ -25,11 +25,13 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 
 #include "fp8gemm.h"
+#include "fp8gemm_testing.h"
 #include "quant8.cuh"
 #include "rows.cuh"
 
@@ -67,6 +69,7 @@ struct Params {
   const float *post_w, *gate, *pre_w;
   int gate_kind;
   float scale, eps;
+  SumWait wait;
 };
 
 // Parameters of columns col .. col + 7: pre_w, and a = post_w times a gate per channel.
@@ -181,12 +184,6 @@ __device__ __forceinline__ void keep8(uint32_t at, const Pair8& p) {
 
 __device__ __forceinline__ Pair8 kept8(uint32_t at) { return pairs_of<true>(load8_shared<true>(at)); }
 
-// The CTAs of a cluster end together: none is gone while another, whose waits may
-// have been given up, still sends to it.
-__device__ __forceinline__ void leave_together() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
 // Most threads of a CTA, and the registers a thread of the backward kernel may
 // use (the forward kernel: 64).  They leave nothing to be kept in local memory:
 // with the stages in shared memory the L1 cache has a few KB, and six words
@@ -213,8 +210,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   // narrow bf16 rows before the sum (8192 x 7168 76.7 us against 87, 32768 x 1024
   // 50.2 against 45.5; 16384 x 1024 FP32 48.1 against 51)
   constexpr bool kLate = kF32 || V == 2;
-  row_sum_init(sm);
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  row_sum_init(sm, rank, P.wait);
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
   const int col0 = rank * S.cols;
   const void* const tensors[2] = {y, h};
@@ -255,7 +252,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   cp_wait<1>();
   if (P.post_w) {
     statistics();
-    row_sum(st, sm, it++, rank, gave_up, err);
+    row_sum(st, sm, it++, rank, P.wait, gave_up, err);
   }
   for (long row = row0; row < S.rows; row += step, ++it) {
     float f = token ? P.scale * __ldg(P.gate + row) : P.scale;
@@ -281,7 +278,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
       if (row + step < S.rows) statistics();
     }
     st[1] = sum2(acc);
-    row_sum(st, sm, it, rank, gave_up, err);
+    row_sum(st, sm, it, rank, P.wait, gave_up, err);
     if (!P.post_w) next_row();
     if constexpr (kLate) src.fetch(tensors, 1);
     // the quantiser takes the negatives of its values
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     }
     at += src.step_bytes;
   }
-  if constexpr (kC > 1) leave_together();
+  if constexpr (kC > 1) sums_leave(gave_up);
 }
 
 // Backward.  Each cluster walks its rows and keeps, per column, the two sums
@@ -338,8 +335,8 @@ __global__ void __maxnreg__(backward_regs(kF32, V))
                                   void* dh, void* dy, float* __restrict__ dgate, float* __restrict__ part, uint32_t* err) {
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ RowSum<4, kC> sm;
-  row_sum_init(sm);
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  row_sum_init(sm, rank, P.wait);
   const long row0 = blockIdx.x / kC, step = gridDim.x / kC;
   const int col0 = rank * S.cols;
   const void* const tensors[4] = {h, y, dz, dh_out};
@@ -382,7 +379,7 @@ __global__ void __maxnreg__(backward_regs(kF32, V))
   };
   cp_wait<1>();
   statistics();
-  row_sum(st, sm, it++, rank, gave_up, err);
+  row_sum(st, sm, it++, rank, P.wait, gave_up, err);
   for (long row = row0; row < S.rows; row += step, ++it) {
     const float gt = token ? __ldg(P.gate + row) : 1.f;
     const float r1 = rms_factor(st[0], inv_h, P.eps);
@@ -415,7 +412,7 @@ __global__ void __maxnreg__(backward_regs(kF32, V))
     src.advance();
     if (row + step < S.rows) statistics();
     st[3] = sum2(du_u);
-    row_sum(st, sm, it, rank, gave_up, err);
+    row_sum(st, sm, it, rank, P.wait, gave_up, err);
     const float m2 = P.post_w ? st[3] * gt * inv_h : 0.f;  // <du u>
     if (dgate && token && rank == 0 && threadIdx.x == 0) dgate[row] = st[3];
     const uint64_t f = both(r2 * gt), um = both(-r2 * m2);
@@ -442,7 +439,7 @@ __global__ void __maxnreg__(backward_regs(kF32, V))
       reinterpret_cast<float4*>(pu)[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
   }
-  if constexpr (kC > 1) leave_together();
+  if constexpr (kC > 1) sums_leave(gave_up);
 }
 
 // Sums of partial rows part[2][P][H] over P.  A CTA takes 32 columns and the
@@ -577,6 +574,14 @@ cudaError_t launch(const Plan& p, void (*kernel)(KArgs...), cudaStream_t stream,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// test hook (fp8g_testing_withhold_sum)
+std::atomic<unsigned> g_test_withhold{kNoCall};
+std::atomic<uint32_t> g_test_limit_us{kSumWaitUs};
+
+SumWait sum_wait() {
+  return SumWait{g_test_withhold.load(std::memory_order_relaxed), g_test_limit_us.load(std::memory_order_relaxed)};
+}
+
 int check_rows(int dtype, int rows, int H, const float* gate, int gate_kind, float scale, float eps) {
   if (dtype != FP8G_IN_BF16 && dtype != FP8G_IN_F32) return FP8G_ERR_INVALID_ARG;
   if (rows < 0 || H <= 0 || H > kMaxH) return FP8G_ERR_INVALID_ARG;
@@ -611,7 +616,7 @@ extern "C" int fp8g_norm_residual(const void* y, const void* h, int dtype, int r
   uint32_t* err = fp8g::device_error_word();
   if (!err) return FP8G_ERR_CUDA;
   const Plan p = forward_plan(rows, H, dtype);
-  const Params P{post_w, gate, pre_w, gate_kind, scale, eps};
+  const Params P{post_w, gate, pre_w, gate_kind, scale, eps, sum_wait()};
   auto go = [&](auto kernel) { return launch(p, kernel, stream, y, h, p.S, P, h_out, z, q, sa, ld_sa, err); };
   auto by_split = [&](auto narrow, auto one, auto two) { return p.vecs == 1 ? go(narrow) : p.ctas == 1 ? go(one) : go(two); };
   cudaError_t e;
@@ -629,6 +634,18 @@ extern "C" int fp8g_norm_residual(const void* y, const void* h, int dtype, int r
     (void)cudaGetLastError();
     return FP8G_ERR_CUDA;
   }
+  return FP8G_OK;
+}
+
+extern "C" int fp8g_testing_withhold_sum(int call, unsigned wait_limit_us) {
+  if (call < 0) {
+    g_test_withhold.store(kNoCall, std::memory_order_relaxed);
+    g_test_limit_us.store(kSumWaitUs, std::memory_order_relaxed);
+    return FP8G_OK;
+  }
+  if (call > 1 || wait_limit_us < 100 || wait_limit_us > kSumWaitUs) return FP8G_ERR_INVALID_ARG;
+  g_test_limit_us.store(wait_limit_us, std::memory_order_relaxed);
+  g_test_withhold.store(static_cast<unsigned>(call), std::memory_order_relaxed);
   return FP8G_OK;
 }
 
@@ -663,7 +680,7 @@ extern "C" int fp8g_norm_residual_backward(const void* dz, const void* dh_out, c
   uint32_t* err = fp8g::device_error_word();
   if (!err) return FP8G_ERR_CUDA;
   const Plan p = backward_plan(rows, H, dtype);
-  const Params P{post_w, gate, pre_w, gate_kind, scale, eps};
+  const Params P{post_w, gate, pre_w, gate_kind, scale, eps, sum_wait()};
   float* part = params ? static_cast<float*>(workspace) : nullptr;
   if (rows > 0) {
     auto go = [&](auto kernel) { return launch(p, kernel, stream, dz, dh_out, h_out, y, p.S, P, dh, dy, dgate, part, err); };

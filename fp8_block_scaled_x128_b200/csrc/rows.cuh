@@ -173,20 +173,33 @@ __device__ __forceinline__ float warp_sums(const float (&v)[2]) {
 // stored to global memory (it cost the backward of 4096 x 7168 FP32 33 us).  A CTA
 // writes a peer's buffer again only after it has the peer's sums of the call in
 // between, which every warp of the peer sends after reading the buffer; and it
-// leaves after all sums sent to it have arrived.
+// leaves after all sums sent to it have arrived (sums_leave).
 template <int n, int kC>
 struct RowSum {
   float s[2][n][16 * kC];
   uint64_t bar[2];
 };
 
-// A wait on a local mbarrier, given up after a second: the flag is recorded, and
-// this thread's later waits return at once (their rows are undefined).
-__device__ __forceinline__ void wait_or_flag(uint32_t bar, uint32_t parity, bool& gave_up, uint32_t* err) {
+// Limit of a cluster's waits, and the test hook that makes one run out: in call
+// `withhold` (0 or 1; kNoCall: none) the last CTA of every cluster waits for an
+// arrival that never comes.
+constexpr uint32_t kSumWaitUs = 1000000;
+constexpr unsigned kNoCall = 0xFFFFFFFFu;
+struct SumWait {
+  unsigned withhold;
+  uint32_t limit_us;
+};
+
+// A wait on a local mbarrier, given up after the limit: the flag is recorded, and
+// this thread neither waits, nor arrives, nor sends any more (its rows are undefined).
+// An arrival on a phase that the last one has left open would be one too many for
+// the barrier, and without this thread's sums its peers give up in turn.
+__device__ __forceinline__ void wait_or_flag(uint32_t bar, uint32_t parity, uint32_t limit_us, bool& gave_up,
+                                             uint32_t* err) {
   if (gave_up || mbar_try_wait_cluster(bar, parity)) return;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait_cluster(bar, parity)) {
-    if (globaltimer_ns() - t0 > 1000000000ull) {
+    if (globaltimer_ns() - t0 > limit_us * 1000ull) {
       gave_up = true;
       atomicOr(err, 0x1u);  // FP8G_DEVERR_TIMEOUT
       return;
@@ -196,18 +209,19 @@ __device__ __forceinline__ void wait_or_flag(uint32_t bar, uint32_t parity, bool
 
 // Before the first row_sum, by all threads; with kC > 1 a cluster barrier has to follow.
 template <int n, int kC>
-__device__ __forceinline__ void row_sum_init(RowSum<n, kC>& sm) {
+__device__ __forceinline__ void row_sum_init(RowSum<n, kC>& sm, int rank, const SumWait& limits) {
   if constexpr (kC > 1) {
     if (threadIdx.x == 0) {
-      mbar_init(smem_u32(&sm.bar[0]), 1);
-      mbar_init(smem_u32(&sm.bar[1]), 1);
+#pragma unroll
+      for (unsigned i = 0; i < 2; ++i) mbar_init(smem_u32(&sm.bar[i]), rank == kC - 1 && i == limits.withhold ? 2 : 1);
       fence_mbar_init();
     }
   }
 }
 
 template <int n, int kC>
-__device__ __forceinline__ void row_sum(float (&v)[n], RowSum<n, kC>& sm, unsigned call, int rank, bool& gave_up, uint32_t* err) {
+__device__ __forceinline__ void row_sum(float (&v)[n], RowSum<n, kC>& sm, unsigned call, int rank, const SumWait& limits,
+                                        bool& gave_up, uint32_t* err) {
   constexpr int kLanes = 32 / n;  // lanes that hold the same value
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   float mine = warp_sums(v);
@@ -219,13 +233,13 @@ __device__ __forceinline__ void row_sum(float (&v)[n], RowSum<n, kC>& sm, unsign
       __syncthreads();
     } else {
       const uint32_t bar = smem_u32(&sm.bar[turn]);
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, kC * nw * n * 4);
-      if (peer < kC)
+      if (threadIdx.x == 0 && !gave_up) mbar_arrive_expect_tx(bar, kC * nw * n * 4);
+      if (peer < kC && !gave_up)
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
                          mapa(smem_u32(&sm.s[turn][value][16 * rank + w]), peer)),
                      "r"(__float_as_uint(mine)), "r"(mapa(bar, peer))
                      : "memory");
-      wait_or_flag(bar, call >> 1 & 1, gave_up, err);
+      wait_or_flag(bar, call >> 1 & 1, limits.limit_us, gave_up, err);
     }
     // the lanes of a value add the warps' sums of it
     float x = 0.f;
@@ -240,6 +254,19 @@ __device__ __forceinline__ void row_sum(float (&v)[n], RowSum<n, kC>& sm, unsign
   }
 #pragma unroll
   for (int i = 0; i < n; ++i) v[i] = __shfl_sync(0xffffffffu, mine, kLanes * i);
+}
+
+// The CTAs of a cluster end together: none is gone while another, whose waits may
+// have been given up, still sends to it.  Behind the barrier everything is sent; a
+// CTA that has given up a wait stays some microseconds longer, since what was sent
+// to it last may still be on its way.
+__device__ __forceinline__ void sums_leave(bool gave_up) {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  if (gave_up) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 20000) {
+    }
+  }
 }
 
 // ---------------------------------------------------------------- asynchronous copies

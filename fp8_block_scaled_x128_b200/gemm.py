@@ -39,6 +39,8 @@ lib.fp8g_quantize_128x128.restype = _I
 lib.fp8g_quantize_128x128.argtypes = [_P, _I, _I, _I, _P, _P, _P]
 lib.fp8g_testing_withhold_stage.restype = _I
 lib.fp8g_testing_withhold_stage.argtypes = [_I, C.c_uint]
+lib.fp8g_testing_withhold_sum.restype = _I
+lib.fp8g_testing_withhold_sum.argtypes = [_I, C.c_uint]
 lib.fp8g_moe_dispatch_workspace_bytes.restype = C.c_size_t
 lib.fp8g_moe_dispatch_workspace_bytes.argtypes = [_I, _I]
 lib.fp8g_moe_dispatch.restype = _I
@@ -138,6 +140,14 @@ def testing_withhold_stage(iteration: int | None, wait_limit_us: int = 2000) -> 
     give up on any wait after `wait_limit_us`; None turns it off."""
     _check(lib.fp8g_testing_withhold_stage(-1 if iteration is None else int(iteration), int(wait_limit_us)),
            "fp8g_testing_withhold_stage")
+
+
+def testing_withhold_sum(call: int | None, wait_limit_us: int = 2000) -> None:
+    """Test hook (include/fp8gemm_testing.h): from the next call on, the last CTA
+    of a norm's cluster waits in exchange `call` (0 or 1) for an arrival that never
+    comes, and waits for sums give up after `wait_limit_us`; None turns it off."""
+    _check(lib.fp8g_testing_withhold_sum(-1 if call is None else int(call), int(wait_limit_us)),
+           "fp8g_testing_withhold_sum")
 
 
 def last_variant() -> int:

@@ -1,5 +1,5 @@
 /*
- * fp8gemm_testing.h -- test hook of libfp8gemm.so.  Not for production use.
+ * fp8gemm_testing.h -- test hooks of libfp8gemm.so.  Not for production use.
  *
  * Every pipeline wait inside the GEMM kernels is bounded: a wait that does
  * not complete within its limit (1 s by default) records FP8G_DEVERR_TIMEOUT
@@ -28,6 +28,17 @@ extern "C" {
  * Returns FP8G_OK, or FP8G_ERR_INVALID_ARG for a limit out of range.
  */
 int fp8g_testing_withhold_stage(int iteration, unsigned wait_limit_us);
+
+/*
+ * The same for fp8g_norm_residual and its gradient where a row takes a cluster
+ * of CTAs: from the next call on, the last CTA of every cluster waits in
+ * exchange `call` (0 or 1: the cluster's first two; about one a row) for an
+ * arrival that never comes, and every wait for sums gives up after
+ * `wait_limit_us` microseconds (100 .. 1000000) instead of 1 s.  Calls that reach that exchange record
+ * FP8G_DEVERR_TIMEOUT and leave their outputs undefined.  A negative `call`
+ * turns the hook off.  Process-wide; returns as above.
+ */
+int fp8g_testing_withhold_sum(int call, unsigned wait_limit_us);
 
 #ifdef __cplusplus
 }

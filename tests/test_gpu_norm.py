@@ -429,3 +429,30 @@ def test_parameter_sums_of_many_rows(g, rows, H, post, gate, dtype):
         assert bool(shown.all()) if gate == "channel" else float(shown.double().mean()) > 0.9   # a token's gate may be near 0
         within(t, each.sum(0), rounded(each.sum(0), bound, torch.float32), name)
     assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("exchange", [0, 1])
+@pytest.mark.parametrize("H,dtype", [(8200, torch.bfloat16), (12416, torch.bfloat16), (16384, torch.float32)],
+                         ids=["2", "2-ragged", "2-and-4"])
+def test_withheld_sums_time_out_and_the_gpu_stays_usable(g, H, dtype, exchange):
+    """One CTA of every cluster waits in one exchange for an arrival that never comes
+    and gives up, and its peers after it: every wait ends at its limit, the call records the timeout, and the same calls without
+    the hook give what they gave before."""
+    rows = 1200
+    x, gen = inputs(H, rows, H, dtype, True, "channel", True, True)
+    dz = torch.randn(rows, H, generator=gen).to(dtype).cuda()
+    y, h = dev(x["y"]), dev(x["h"])
+    kw = dict(post_weight=dev(x["post_w"]), gate=dev(x["gate"]), scale=0.5, pre_weight=dev(x["pre_w"]), eps=EPS)
+    calls = [lambda: g.norm_residual(y, h, **kw), lambda: g.norm_residual_backward(dz, None, h, y, **kw)]
+    for run in calls:
+        want = run()
+        assert g.device_error(clear=True) == 0
+        g.testing_withhold_sum(exchange, wait_limit_us=2000)
+        try:
+            run()
+            torch.cuda.synchronize()    # raises if the kernel faulted
+        finally:
+            g.testing_withhold_sum(None)
+        assert g.device_error(clear=True) == g.DEVERR_TIMEOUT
+        assert all(torch.equal(a, b) for a, b in zip(want, run()))
+        assert g.device_error() == 0

@@ -235,3 +235,10 @@ def test_binding_takes_slots_of_any_shape(gemm):
             gemm.moe_permute_backward(fake((128, 64)), bad, 4, 2)
         with pytest.raises(TypeError, match="pos"):
             gemm.moe_combine_backward(x, fake((128, 256)), bad, None, 4, 2)
+
+
+def test_withheld_sum_hook_checks_its_arguments(gemm):
+    f = gemm.lib.fp8g_testing_withhold_sum
+    assert f(1, 50) == f(1, 2_000_000) == INVALID     # limits below 100 us and above 1 s
+    assert f(2, 2000) == INVALID                      # an exchange that the hook does not reach
+    assert f(1, 2000) == OK and f(-1, 0) == OK        # on, and off again
