@@ -547,11 +547,27 @@ Plan forward_plan(int rows, int H, int dtype) {
 
 // At least 4 rows a cluster once one launch could not add the partial rows of all
 // (1000 x 512 FP32: 9.2 us against 10.7 with a row each).
-Plan backward_plan(int rows, int H, int dtype) {
+Plan backward_plan(int rows, int H, int dtype, long most_clusters = LONG_MAX) {
   const int vecs = H <= kNarrow ? 1 : 2;
   const bool f32 = dtype == FP8G_IN_F32;
   return plan_of(rows, H, f32 ? 4 : 2, 4, 8, vecs, threads_at(backward_regs(f32, vecs)),
-                 std::max<long>(kOneLaunch, rows / 4));
+                 std::min(most_clusters, std::max<long>(kOneLaunch, rows / 4)));
+}
+
+// The launch of a plan; attr is the caller's.
+cudaLaunchConfig_t config(const Plan& p, cudaLaunchAttribute* attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.clusters * p.ctas), 1, 1);
+  cfg.blockDim = dim3(p.threads, 1, 1);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = p.ctas;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.ctas > 1 ? 1 : 0;
+  return cfg;
 }
 
 // Launches the kernel for the plan's cluster size.
@@ -559,19 +575,28 @@ template <typename... KArgs, typename... Args>
 cudaError_t launch(const Plan& p, void (*kernel)(KArgs...), cudaStream_t stream, Args... args) {
   const cudaError_t e = fp8g::rows::allow_smem(kernel);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(p.clusters * p.ctas), 1, 1);
-  cfg.blockDim = dim3(p.threads, 1, 1);
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.ctas > 1 ? 1 : 0;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = config(p, &attr, stream);
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Clusters of 4 CTAs that the current device runs at once, 0 if it does not say.
+// A quarter of its SMs is too many: a GPC's SMs beyond a multiple of four hold none
+// (pairs always fit), and a cluster that does not fit starts when the others have
+// walked all their rows (33 fit; 4096 x 16384 FP32: 573 us with 37, 331 with 33).
+// All plans of 4 CTAs take an SM for each CTA, so one answer per device serves them.
+int quad_clusters(const Plan& p) {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  auto kernel = norm_residual_backward_kernel<true, 2, 4>;
+  if (fp8g::rows::allow_smem(kernel) != cudaSuccess) return 0;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = config(p, &attr, nullptr);
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // test hook (fp8g_testing_withhold_sum)
@@ -679,7 +704,15 @@ extern "C" int fp8g_norm_residual_backward(const void* dz, const void* dh_out, c
   if (rows == 0 && !params) return FP8G_OK;
   uint32_t* err = fp8g::device_error_word();
   if (!err) return FP8G_ERR_CUDA;
-  const Plan p = backward_plan(rows, H, dtype);
+  Plan p = backward_plan(rows, H, dtype);
+  if (p.ctas == 4) {
+    const int fit = quad_clusters(p);
+    if (fit < 1) {
+      (void)cudaGetLastError();
+      return FP8G_ERR_CUDA;
+    }
+    p = backward_plan(rows, H, dtype, fit);
+  }
   const Params P{post_w, gate, pre_w, gate_kind, scale, eps, sum_wait()};
   float* part = params ? static_cast<float*>(workspace) : nullptr;
   if (rows > 0) {
