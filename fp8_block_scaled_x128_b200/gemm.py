@@ -370,7 +370,7 @@ def _operand(t, dt, shape, index, name):
 
 def _slots(t, R, index, name):
     """t, if it is a contiguous int32 CUDA tensor of R routed slots, flat or [T, topk]."""
-    return _operand(t, torch.int32, t.shape if math.prod(t.shape) == R else (R,), index, name)
+    return _operand(t, torch.int32, (R,) if t.dim() == 1 or math.prod(t.shape) != R else t.shape, index, name)
 
 
 def _rows(t, name):
