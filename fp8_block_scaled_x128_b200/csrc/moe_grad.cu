@@ -20,6 +20,11 @@
 // shared memory.  Reading pos (4 bytes a slot) once per such CTA costs little
 // next to rows of some thousand columns, and saves the workspace, the launches
 // and the atomics on memory that a map from rows to slots would need.
+//
+// Times in this file: calls back to back as a program makes them, into outputs of
+// their own and for long enough that the power cap acts; "replayed" means the
+// same calls in a short CUDA graph at full clock, whose outputs stay in L2 in part.
+// Comparisons of two forms are replayed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -109,9 +114,9 @@ __device__ __forceinline__ void pad_range(int cta, int pads, int blocks, int& b0
 // work behind when the last ones run (with a CTA per token, 3.5 waves of 8 CTAs
 // an SM, the last wave ran half empty).  pos and m_indices are read by coherent loads
 // (and pos is not __restrict__): the layout kernel still writes them when this one
-// starts.  4096 tokens x top-8 over 64 experts, 7168
-// bf16: 101 us with the layout kernel (of which some 7 us are not hidden), 588 MB
-// with the padding rows: 0.89 of the measured copy bandwidth.
+// starts.  4096 tokens x top-8 over 64 experts, 7168 bf16: 104 us with the layout
+// kernel (of which some 7 us are not hidden), 588 MB with the padding rows: 0.87 of
+// the measured copy bandwidth (replayed 101).
 template <int kCap>
 __global__ void __launch_bounds__(256) moe_permute_kernel(const uint4* __restrict__ x, int vecs, int parts, int tokens, int T,
                                                           int topk, const int32_t* pos, uint4* __restrict__ xs, int M,
@@ -245,8 +250,8 @@ __global__ void __launch_bounds__(256) moe_permute_direct_kernel(const uint4* __
 }
 
 // A CTA per token: all of a thread's row loads are issued before the first
-// addition, which run in slot order.  The rows above, 529 MB: 77 us, 1.05 of the
-// measured copy bandwidth (reads outweigh writes, part of which stay in L2).
+// addition, which run in slot order.  The rows above, 529 MB: 85 us, 0.95 of the
+// measured copy bandwidth (replayed 77: part of what it writes stays in L2).
 template <bool kF32, int kCap>
 __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* __restrict__ dxs, int N,
                                                                    const int32_t* __restrict__ pos, int T, int topk,
@@ -280,9 +285,12 @@ __global__ void __launch_bounds__(256) moe_permute_backward_kernel(const void* _
 // a thread), four slots at a time.  A thread copies its own vectors of the next
 // four slots' D rows (and of dout) into shared memory (cp.async) before it works
 // on the current ones, so loads are under way all the time without holding
-// registers.  The same rows, 1.06 GB with the padding: 171 us to bf16, 0.94 of the
-// measured copy bandwidth; 0.80 GB to codes: 141 us, 0.86, with 60 % of the issue
-// slots used (packed FP32x2 arithmetic throughout).
+// registers.  The same rows, 1.06 GB with the padding: 174 us to bf16, 0.93 of the
+// measured copy bandwidth; 0.80 GB to codes: 161 us, 0.76, replayed 141.  To codes
+// nothing is saturated: 26 warps an SM issue in 65 % of the cycles, DRAM is at
+// 64 %, and the 10.1 cycles between two instructions of a warp are spread over fixed
+// latencies (1.8), waiting to be selected (1.7), the FP32 pipe (1.3), shared memory
+// and shuffles (1.3), barriers (1.0) and loads (0.9); packed FP32x2 throughout.
 //
 // kQuant: the rows leave as e4m3 codes and 1x128 scales; 16 lanes hold a group
 // of columns.  Its largest |w x| is |w| times its largest |x|, rounded once

@@ -15,9 +15,10 @@
 // experts of the slots before it (a ballot per slot and 32 earlier slots),
 // instead of waiting for a layout kernel; one more CTA counts the experts' rows.
 // The counting grows with T * T * topk * topk, so larger batches run the layout
-// kernel first.  K = 7168, top-8, bf16: one token 2.7 us and 256 tokens 7.4 us
-// (chains of three loads, the counting and the codes; 18.8 MB), 512 tokens 11 us,
-// 1024 tokens with the layout kernel 21 us (75 MB, 0.54 of the copy bandwidth).
+// kernel first.  K = 7168, top-8, bf16, calls back to back (and replayed in a CUDA
+// graph): one token 9.3 us (2.7) and 256 tokens 9.5 (7.4; chains of three loads, the
+// counting and the codes; 18.8 MB), 512 tokens 12.3 (11.1), 1024 tokens with the
+// layout kernel 23.5 (21; 75 MB, 0.49 of the copy bandwidth).
 #include <cuda_runtime.h>
 
 #include <algorithm>

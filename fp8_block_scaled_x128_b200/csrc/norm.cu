@@ -22,6 +22,11 @@
 // pass starts from the stored h'.  Both row statistics of the backward pass
 // are recomputed from h' and y, which it has to read anyway, so nothing is
 // kept between the passes.
+//
+// Times in this file: calls back to back as a program makes them, into outputs of
+// their own and for long enough that the power cap acts; "replayed" means the
+// same calls in a short CUDA graph at full clock, whose outputs stay in L2 in part.
+// Comparisons of two forms are replayed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -194,12 +199,15 @@ constexpr int backward_regs(bool f32, int vecs) { return vecs == 2 ? 128 : f32 ?
 constexpr int threads_at(int regs) { return 128 * (16384 / (32 * regs)); }
 
 // Forward.  Each element of y and h is read once and each of h' and z written
-// once.  8192 x 7168 bf16 with post-norm and channel gate: 76.7 us, 6.1 TB/s, 0.93
-// of the measured copy bandwidth (32768 x 1024: 45.5 us, 0.90; 4096 x 16384: 89 us,
-// 0.92); two CTAs share an SM, so that one computes while the other waits for a
-// sum.  With codes out 84 us, 0.75: the quantisation adds a third to the
-// instructions, and the issue slots and the sum's latency bound it.  One row of
-// 7168, decode's form: 4.2 us, two sums' latencies behind one load.
+// once.  8192 x 7168 bf16 with post-norm and channel gate: 80 us, 5.9 TB/s, 0.90 of
+// the measured copy bandwidth, replayed 76.7 (32768 x 1024: 47 us, 0.87; 4096 x 16384:
+// 94 us, 0.87; 4096 x 7168 FP32: 86 us, 0.83); two CTAs share an SM, so that one
+// computes while the other waits for a sum.  With codes out 90 us, 0.70, replayed
+// 84: the quantisation adds a third to the instructions.  There 26 warps an SM
+// fill 63 % of the issue slots and no one stall leads: of the 10.2 cycles between two
+// instructions of a warp 2.3 are shared memory and shuffles, 2.0 fixed latencies,
+// 0.7 barriers, 0.6 loads.  One row of 7168, decode's form: 10.5 us a call, 4.3
+// replayed: two sums' latencies behind one load.
 template <bool kF32, int V, int kC, bool kQuant>
 __global__ void __launch_bounds__(kMaxThreads, 2)
     norm_residual_kernel(const void* y, const void* h, Shape S, Params P, void* h_out, void* z, uint8_t* q, float* sa,
@@ -324,11 +332,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
 // dh needs the row's statistics, and dy a sum over the row of a dh u, which is
 // exchanged with the next row's statistics.
 //
-// 8192 x 7168 bf16: 115.5 us with the parameter sums, 6.1 TB/s, 0.93 of the measured
-// copy bandwidth (8192 x 8192: 131 us, 0.94; 32768 x 1024: 76 us, 0.81; 4096 x 16384:
-// 144 us, 0.86; 4096 x 7168 FP32: 131 us, 0.82), at 14 warps an SM of 128 registers.
-// Narrower rows are bound by instructions issued, a few rows by the launches and
-// the latency of load, sum and store (400 x 2112 FP32: 12.9 us).
+// 8192 x 7168 bf16: 130 us with the parameter sums, 5.4 TB/s, 0.83 of the measured
+// copy bandwidth, replayed 116, 0.93 (8192 x 8192: 140 us, 0.88; 32768 x 1024: 82 us,
+// 0.75; 4096 x 16384: 156 us, 0.79; 4096 x 7168 FP32: 138 us, 0.78; 4096 x 16384
+// FP32: 334 us, 0.74), at 14 warps an SM of 128 registers.  A few rows are bound by
+// latency: 1021 x 2112 FP32, 23 us a call and 19.4 replayed, has 9 warps an SM that
+// issue in 21 % of the cycles and wait for shared memory and loads 6 cycles of 10,
+// with 108 SMs at 8 rows and 40 at 4, and then the parameter sums on 66 CTAs
+// (7 us with cold caches).  400 x 2112 FP32: 12.8 us replayed.
 template <bool kF32, int V, int kC>
 __global__ void __maxnreg__(backward_regs(kF32, V))
     norm_residual_backward_kernel(const void* dz, const void* dh_out, const void* h, const void* y, Shape S, Params P,

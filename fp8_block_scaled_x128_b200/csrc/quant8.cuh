@@ -1,6 +1,7 @@
 // quant8.cuh -- quantisation of 8 values of a 1x128 group whose largest
-// magnitude is known: the codes and scale of quant_impl.cuh's definition, bit
-// for bit, at fewer instructions.
+// magnitude is known: for finite values the codes and scale of quant_impl.cuh's
+// definition, bit for bit, at fewer instructions (a group with an infinite value
+// gets a NaN scale here, an infinite one there; its codes are NaN in both).
 //
 //   scale = fl(amax / 448) (1 where that is zero), code = e4m3(fl(x / scale))
 //
